@@ -29,3 +29,4 @@ from .paged_attention import (  # noqa: F401
 )
 from .kv_manager import KvManager, KvManagerError, NoBlocks  # noqa: F401,E402
 from . import sampler  # noqa: F401,E402
+from . import drafting  # noqa: F401,E402

@@ -14,16 +14,19 @@ import numpy as np
 from . import _abi
 from ._abi import (PA_DEV_ERR_BLOCK_ID, PA_DEV_ERR_CONTEXT, PA_DEV_ERR_SLOT,  # noqa: F401
                    PA_DEV_ERR_TIMEOUT, PA_KERNEL_AUTO, PA_KERNEL_SIMT, PA_KERNEL_TCGEN05,
-                   PA_PREFILL_EXACT_WEIGHTS, PaError, PoolDesc)
+                   PA_PREFILL_EXACT_WEIGHTS, PA_ROPE_SCALE_BASE, PA_ROPE_SCALE_LINEAR,
+                   PA_ROPE_SCALE_NONE, PA_ROPE_SCALE_RAMP, PaError, PoolDesc)
 
 __all__ = [
     "pa_reshape_and_cache", "pa_copy_blocks", "pa_decode", "pa_decode_workspace_size",
     "pa_decode_noalloc",
     "pa_chunked_prefill", "pa_gather_kv", "pa_get_device_error", "pa_sample", "pa_swap_blocks",
     "pa_read_probe",
+    "pa_rope", "pa_rope_and_cache", "pa_rope_frequencies",
     "pool_desc", "lib",
     "PaError", "PA_KERNEL_AUTO", "PA_KERNEL_SIMT", "PA_KERNEL_TCGEN05",
     "PA_PREFILL_EXACT_WEIGHTS",
+    "PA_ROPE_SCALE_NONE", "PA_ROPE_SCALE_LINEAR", "PA_ROPE_SCALE_BASE", "PA_ROPE_SCALE_RAMP",
 ]
 
 
@@ -295,3 +298,142 @@ def pa_read_probe(k_pool, v_pool, block_tables, context_lens, num_ctas=None, out
         _ptr(k_pool), _ptr(v_pool), pool_desc(k_pool), _ptr(block_tables), block_tables.shape[1],
         _ptr(context_lens), context_lens.shape[0], _ptr(out), int(num_ctas), _stream(stream)))
     return out
+
+
+# ----------------------------------------------------------------------------
+# Drafting and eviction (include/pa_rope.h)
+#
+# These calls run on the device their tensors are on (whatever the current one)
+# and, without a `stream`, on that device's current stream; what they allocate
+# belongs to the stream they run on.
+# ----------------------------------------------------------------------------
+def _arg(name, t, dtype, device, shape=None, contiguous=True):
+    """Check one tensor argument; ``shape``: sizes it must have, None where any."""
+    if not isinstance(t, _torch().Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if shape is not None:
+        have = t.shape
+        if len(have) != len(shape) or any(w is not None and h != w for h, w in zip(have, shape)):
+            want = ", ".join("*" if w is None else str(w) for w in shape)
+            raise ValueError(f"{name} must have shape [{want}], got {list(have)}")
+
+
+def _rows_arg(name, t, device, shape):
+    """A bf16 [T, H, D] tensor whose heads are packed; returns its token stride."""
+    _arg(name, t, _torch().bfloat16, device, shape, contiguous=False)
+    tokens, heads, dim = t.shape
+    stride, by_head, by_dim = t.stride()
+    if (by_dim != 1 and dim > 1) or (by_head != dim and heads > 1):
+        raise ValueError(f"{name} must be [T, H, D] with packed heads")
+    return stride if tokens > 1 else max(stride, heads * dim)
+
+
+def _empty(shape, dtype, device, stream):
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _run(name, device, stream, *args):
+    """Call ``name`` of the library with the stream's handle as its last argument."""
+    torch = _torch()
+    fn = getattr(_abi.load(), name)
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(device.index)
+    else:
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        handle = stream.cuda_stream
+    if device.index == torch.cuda.current_device():
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, handle)
+    if status:
+        _abi.check(name, status)
+
+
+def pa_rope_frequencies(rot_dim, base=10000.0, scaling=_abi.PA_ROPE_SCALE_NONE, scale=1.0,
+                        original_max_position=0.0, low_turns=1.0, high_turns=32.0):
+    """Inverse frequencies (NumPy float64 [rot_dim / 2]) and the factor that goes with
+    them, for ``pa_rope``; ``scaling``: one of ``PA_ROPE_SCALE_*``."""
+    out = np.empty(max(int(rot_dim), 0) // 2, np.float64)
+    factor = ctypes.c_double(1.0)
+    _abi.check("pa_rope_frequencies", lib().pa_rope_frequencies(
+        int(rot_dim), float(base), int(scaling), float(scale), float(original_max_position),
+        float(low_turns), float(high_turns), out.ctypes.data_as(ctypes.c_void_p),
+        ctypes.byref(factor)))
+    return out, factor.value
+
+
+def pa_rope(q, k, positions, inv_freq, interleaved=False, factor=1.0, q_out=None, k_out=None,
+            stream=None):
+    """Rotate ``q`` (bf16 [T, Hq, D]) and ``k`` (bf16 [T, Hkv, D], or None) by their
+    tokens' ``positions`` (int64 [T]) and ``inv_freq`` (float64 [rot_dim / 2]; the
+    first ``rot_dim`` dims of a head are rotated).  ``q_out`` / ``k_out`` may be the
+    inputs.  Returns ``(q_out, k_out)``."""
+    torch = _torch()
+    dev = q.device
+    qs = _rows_arg("q", q, dev, (None, None, None))
+    tokens, hq, d = q.shape
+    _arg("positions", positions, torch.int64, dev, (tokens,))
+    _arg("inv_freq", inv_freq, torch.float64, dev, (None,))
+    if q_out is None:
+        q_out = _empty((tokens, hq, d), torch.bfloat16, dev, stream)
+    qos = _rows_arg("q_out", q_out, dev, (tokens, hq, d))
+    hkv = ks = kos = 0
+    if k is not None:
+        ks = _rows_arg("k", k, dev, (tokens, None, d))
+        hkv = k.shape[1]
+        if k_out is None:
+            k_out = _empty((tokens, hkv, d), torch.bfloat16, dev, stream)
+        kos = _rows_arg("k_out", k_out, dev, (tokens, hkv, d))
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    _run("pa_rope", dev, stream, q.data_ptr(), qs, q_out.data_ptr(), qos, hq, _ptr(k), ks,
+         _ptr(k_out), kos, hkv, d, positions.data_ptr(), inv_freq.data_ptr(),
+         2 * inv_freq.shape[0], int(bool(interleaved)), float(factor), tokens)
+    return q_out, k_out
+
+
+def pa_rope_and_cache(q, key, value, k_pool, v_pool, slot_mapping, positions, inv_freq,
+                      interleaved=False, factor=1.0, q_weight=None, k_weight=None, eps=1e-6,
+                      q_out=None, stream=None):
+    """Norm each head of ``q`` and ``key`` (where a bf16 [D] weight is given), rotate
+    them as ``pa_rope`` does, write the prepared key and ``value`` into the pools at
+    ``slot_mapping`` (int64 [T]; negative = skip) and return the prepared q
+    (``q_out`` may be ``q``)."""
+    torch = _torch()
+    dev = q.device
+    bf16 = torch.bfloat16
+    _arg("k_pool", k_pool, bf16, dev, (None, None, None, None))
+    _arg("v_pool", v_pool, bf16, dev, k_pool.shape)
+    hkv, d = k_pool.shape[1], k_pool.shape[3]
+    qs = _rows_arg("q", q, dev, (None, None, d))
+    tokens, hq, _ = q.shape
+    ks = _rows_arg("key", key, dev, (tokens, hkv, d))
+    vs = _rows_arg("value", value, dev, (tokens, hkv, d))
+    _arg("slot_mapping", slot_mapping, torch.int64, dev, (tokens,))
+    _arg("positions", positions, torch.int64, dev, (tokens,))
+    _arg("inv_freq", inv_freq, torch.float64, dev, (None,))
+    if q_weight is not None:
+        _arg("q_weight", q_weight, bf16, dev, (d,))
+    if k_weight is not None:
+        _arg("k_weight", k_weight, bf16, dev, (d,))
+    if q_out is None:
+        q_out = _empty((tokens, hq, d), bf16, dev, stream)
+    qos = _rows_arg("q_out", q_out, dev, (tokens, hq, d))
+    _run("pa_rope_and_cache", dev, stream, q.data_ptr(), qs, q_out.data_ptr(), qos, hq,
+         key.data_ptr(), ks, value.data_ptr(), vs, _ptr(q_weight), _ptr(k_weight), float(eps),
+         positions.data_ptr(), inv_freq.data_ptr(), 2 * inv_freq.shape[0],
+         int(bool(interleaved)), float(factor), k_pool.data_ptr(), v_pool.data_ptr(),
+         pool_desc(k_pool), slot_mapping.data_ptr(), tokens)
+    return q_out

@@ -33,10 +33,18 @@ PA_KERNEL_SIMT = 1
 PA_KERNEL_TCGEN05 = 2
 PA_PREFILL_EXACT_WEIGHTS = 0x1
 
+PA_ROPE_HALF = 0
+PA_ROPE_INTERLEAVED = 1
+PA_ROPE_SCALE_NONE = 0
+PA_ROPE_SCALE_LINEAR = 1
+PA_ROPE_SCALE_BASE = 2
+PA_ROPE_SCALE_RAMP = 3
+
 PA_NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024
 
 # Every entry point of include/pa.h, with its ctypes signature.
 c_int, c_i32, c_i64, c_f32 = ctypes.c_int, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+c_f64 = ctypes.c_double
 c_vp, c_size = ctypes.c_void_p, ctypes.c_size_t
 
 
@@ -89,6 +97,13 @@ SIGNATURES = {
     "pa_kvm_num_free_host_blocks": (c_i32, [c_vp]),
     # block swapping (include/pa_swap.h)
     "pa_swap_blocks": (c_int, [c_vp, c_vp, PoolDesc, c_vp, c_vp, c_i32, c_vp, c_i32, c_i32, c_vp]),
+    # rotary positions, head norms and the cache write (include/pa_rope.h)
+    "pa_rope": (c_int, [c_vp, c_i64, c_vp, c_i64, c_i32, c_vp, c_i64, c_vp, c_i64, c_i32, c_i32,
+                        c_vp, c_vp, c_i32, c_i32, c_f32, c_i32, c_vp]),
+    "pa_rope_and_cache": (c_int, [c_vp, c_i64, c_vp, c_i64, c_i32, c_vp, c_i64, c_vp, c_i64, c_vp,
+                                  c_vp, c_f32, c_vp, c_vp, c_i32, c_i32, c_f32, c_vp, c_vp,
+                                  PoolDesc, c_vp, c_i32, c_vp]),
+    "pa_rope_frequencies": (c_int, [c_i32, c_f64, c_i32, c_f64, c_f64, c_f64, c_f64, c_vp, c_vp]),
     # paged read-bandwidth probe (include/pa_probe.h)
     "pa_read_probe": (c_int, [c_vp, c_vp, PoolDesc, c_vp, c_i32, c_vp, c_i32, c_vp, c_i32, c_vp]),
 }
