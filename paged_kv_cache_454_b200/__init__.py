@@ -34,9 +34,15 @@ def lib():
     return _abi.load()
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t) -> int | None:
@@ -308,26 +314,38 @@ def pa_read_probe(k_pool, v_pool, block_tables, context_lens, num_ctas=None, out
 # belongs to the stream they run on.
 # ----------------------------------------------------------------------------
 def _arg(name, t, dtype, device, shape=None, contiguous=True):
-    """Check one tensor argument; ``shape``: sizes it must have, None where any."""
+    """Check one tensor argument (``shape``: the sizes it must have).  One pass of
+    cheap comparisons; the words for what is wrong are found only then."""
+    try:
+        if (t.dtype is dtype and t.get_device() == device.index
+                and (shape is None or t.shape == shape)
+                and (not contiguous or t.is_contiguous())):
+            return
+    except AttributeError:
+        pass
     if not isinstance(t, _torch().Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if shape is not None:
-        have = t.shape
-        if len(have) != len(shape) or any(w is not None and h != w for h, w in zip(have, shape)):
-            want = ", ".join("*" if w is None else str(w) for w in shape)
-            raise ValueError(f"{name} must have shape [{want}], got {list(have)}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _rows_arg(name, t, device, shape):
+def _dims(name, t, dims):
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got shape {list(t.shape)}")
+
+
+def _rows_arg(name, t, device, shape=None):
     """A bf16 [T, H, D] tensor whose heads are packed; returns its token stride."""
     _arg(name, t, _torch().bfloat16, device, shape, contiguous=False)
-    tokens, heads, dim = t.shape
+    if shape is None:
+        _dims(name, t, 3)
+        shape = t.shape
+    tokens, heads, dim = shape
     stride, by_head, by_dim = t.stride()
     if (by_dim != 1 and dim > 1) or (by_head != dim and heads > 1):
         raise ValueError(f"{name} must be [T, H, D] with packed heads")
@@ -382,17 +400,20 @@ def pa_rope(q, k, positions, inv_freq, interleaved=False, factor=1.0, q_out=None
     inputs.  Returns ``(q_out, k_out)``."""
     torch = _torch()
     dev = q.device
-    qs = _rows_arg("q", q, dev, (None, None, None))
+    qs = _rows_arg("q", q, dev)
     tokens, hq, d = q.shape
     _arg("positions", positions, torch.int64, dev, (tokens,))
-    _arg("inv_freq", inv_freq, torch.float64, dev, (None,))
+    _arg("inv_freq", inv_freq, torch.float64, dev)
+    _dims("inv_freq", inv_freq, 1)
     if q_out is None:
         q_out = _empty((tokens, hq, d), torch.bfloat16, dev, stream)
     qos = _rows_arg("q_out", q_out, dev, (tokens, hq, d))
     hkv = ks = kos = 0
     if k is not None:
-        ks = _rows_arg("k", k, dev, (tokens, None, d))
+        ks = _rows_arg("k", k, dev)
         hkv = k.shape[1]
+        if k.shape != (tokens, hkv, d):
+            raise ValueError(f"k must be [{tokens}, Hkv, {d}], got {list(k.shape)}")
         if k_out is None:
             k_out = _empty((tokens, hkv, d), torch.bfloat16, dev, stream)
         kos = _rows_arg("k_out", k_out, dev, (tokens, hkv, d))
@@ -414,16 +435,21 @@ def pa_rope_and_cache(q, key, value, k_pool, v_pool, slot_mapping, positions, in
     torch = _torch()
     dev = q.device
     bf16 = torch.bfloat16
-    _arg("k_pool", k_pool, bf16, dev, (None, None, None, None))
+    _arg("k_pool", k_pool, bf16, dev)
+    _dims("k_pool", k_pool, 4)
     _arg("v_pool", v_pool, bf16, dev, k_pool.shape)
-    hkv, d = k_pool.shape[1], k_pool.shape[3]
-    qs = _rows_arg("q", q, dev, (None, None, d))
-    tokens, hq, _ = q.shape
+    qs = _rows_arg("q", q, dev)
+    tokens, hq, d = q.shape
+    desc = pool_desc(k_pool)
+    hkv = desc.num_kv_heads
+    if desc.head_dim != d:
+        raise ValueError(f"q has head_dim {d}, the pools {desc.head_dim}")
     ks = _rows_arg("key", key, dev, (tokens, hkv, d))
     vs = _rows_arg("value", value, dev, (tokens, hkv, d))
     _arg("slot_mapping", slot_mapping, torch.int64, dev, (tokens,))
     _arg("positions", positions, torch.int64, dev, (tokens,))
-    _arg("inv_freq", inv_freq, torch.float64, dev, (None,))
+    _arg("inv_freq", inv_freq, torch.float64, dev)
+    _dims("inv_freq", inv_freq, 1)
     if q_weight is not None:
         _arg("q_weight", q_weight, bf16, dev, (d,))
     if k_weight is not None:
@@ -435,5 +461,5 @@ def pa_rope_and_cache(q, key, value, k_pool, v_pool, slot_mapping, positions, in
          key.data_ptr(), ks, value.data_ptr(), vs, _ptr(q_weight), _ptr(k_weight), float(eps),
          positions.data_ptr(), inv_freq.data_ptr(), 2 * inv_freq.shape[0],
          int(bool(interleaved)), float(factor), k_pool.data_ptr(), v_pool.data_ptr(),
-         pool_desc(k_pool), slot_mapping.data_ptr(), tokens)
+         desc, slot_mapping.data_ptr(), tokens)
     return q_out

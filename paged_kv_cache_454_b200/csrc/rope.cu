@@ -1,14 +1,17 @@
 // Rotary positions, norms per head and the cache write of the prepared K and V.
 //
-// One CTA works on the head rows of one token (or a part of them: blockIdx.y).
 // A row of D dims belongs to D/8 neighbouring lanes, 16 bytes each, so a row is
 // read and written with one coalesced access per lane and its norm is a
-// shuffle reduction inside those lanes.  The token's cos and sin are computed
-// once per CTA (one pair per thread) and then stay in registers, a lane always
-// having the same dims whatever the head: per row there is nothing left but the
-// load, the norm, the products and the store.  In the half layout a lane's
-// partner dims are rot/16 lanes away and come by shuffle, in the interleaved
-// layout a pair is inside the lane.
+// shuffle reduction inside those lanes.  A CTA works on four tokens, 64 threads
+// each, and on one part of their rows: the q heads (split further where there
+// are few tokens), the K heads or the V heads, so no part waits for another's
+// loads.  The tokens' cos and sin are computed once per CTA, a pair per thread,
+// and met in shared memory.  A lane always has the same dims whatever the head,
+// so it then keeps its cos and sin, times the norm's weights, in registers, and
+// a row is
+//     y = r (x A + x' B),   r = 1 / sqrt(mean x^2 + eps) or 1,
+// with x' the partner dims: rot/16 lanes away in the half layout (shuffled as
+// packed bf16 pairs), inside the lane in the interleaved one.
 //
 // Bound: HBM for many tokens (every row is read once and written once), the
 // launch for few.
@@ -23,8 +26,16 @@
 namespace pa {
 namespace {
 
+// Measured (graph replays; 32768 tokens of 64/8 heads, 1.34 GB | 4288 of 40/8 |
+// 128 of 64/8): four tokens of a CTA 231 | 28.1 | 3.8 us (5.8 TB/s at the
+// largest), two 271 | 35 | 4.3, one 401 | 63 | 5.2 -- a CTA's angles and its
+// wait for them cost as much as a dozen rows.  Three rows in flight 231 | 28.1,
+// two 238 | 28.1, four 236 | 28.2; four CTAs resident per SM 231, three 251.
 constexpr int kRopeThreads = 256;
-constexpr int kRopeUnroll = 2;  // rows of a lane group in flight
+constexpr int kRopeTokens = 4;  // tokens of a CTA
+constexpr int kRopeTokenThreads = kRopeThreads / kRopeTokens;
+constexpr int kRopeCtasPerSm = 2;  // fewer q CTAs than this: the q heads are split
+constexpr int kRopeRows = 3;       // rows of a lane group in flight
 
 struct RopeParams {
   const uint4* q;
@@ -40,7 +51,9 @@ struct RopeParams {
   const int64_t* positions;
   const double* inv_freq;
   const int64_t* slots;
-  int hq, hkv, rows;  // rows of a token: q heads, K heads and, with the cache write, V heads
+  int hq, hkv;
+  int num_tokens;
+  int q_parts, parts;  // CTAs of four tokens: for their q heads, in all
   int rot;
   int num_blocks;
   float factor, eps;
@@ -59,158 +72,160 @@ __device__ __forceinline__ float2 turn_of(int64_t position, double inv_freq, flo
   return make_float2(c * factor, s * factor);
 }
 
-__device__ __forceinline__ void unpack8(uint4 w, float (&x)[8]) {
-  x[0] = bf16lo(w.x);
-  x[1] = bf16hi(w.x);
-  x[2] = bf16lo(w.y);
-  x[3] = bf16hi(w.y);
-  x[4] = bf16lo(w.z);
-  x[5] = bf16hi(w.z);
-  x[6] = bf16lo(w.w);
-  x[7] = bf16hi(w.w);
-}
+__device__ __forceinline__ float2 unpack2(uint32_t w) { return make_float2(bf16lo(w), bf16hi(w)); }
 
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+__device__ __forceinline__ uint32_t pack2(float2 x) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(x.x, x.y);
   return *reinterpret_cast<const uint32_t*>(&b);
 }
 
+__device__ __forceinline__ uint32_t word(const uint4& w, int j) {
+  return j == 0 ? w.x : j == 1 ? w.y : j == 2 ? w.z : w.w;
+}
+
 template <int D, bool kInterleaved, bool kCache>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kLanes = D / 8;                       // lanes of a row
-  constexpr int kGroups = kRopeThreads / kLanes;      // rows in work at once
-  __shared__ float2 turn[D / 2];
+  constexpr int kGroups = kRopeTokenThreads / kLanes;  // rows of a token in work at once
+  __shared__ float2 turn[kRopeTokens][D / 2];
   // a decode plan launched after this kernel may start now (it reads only the
   // tables and lengths, and waits for this grid before it completes)
   if (kCache) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int64_t t = blockIdx.x;
-  const int lane = threadIdx.x % kLanes;
-  const int group = threadIdx.x / kLanes;
-  const int step = kGroups * gridDim.y;
+  const int mine = threadIdx.x / kRopeTokenThreads;  // which of the CTA's tokens
+  const int at = threadIdx.x % kRopeTokenThreads;
+  const int part = blockIdx.x % p.parts;
+  const int64_t t = static_cast<int64_t>(blockIdx.x / p.parts) * kRopeTokens + mine;
+  const bool live = t < p.num_tokens;  // alike in a warp
+  const int lane = at % kLanes;
+  const bool is_q = part < p.q_parts;
+  const int lead = is_q ? part * kGroups : 0;  // the first head of the token's first group
+  const int first = lead + at / kLanes;        // and of this thread's group
+  const int step = kGroups * (is_q ? p.q_parts : 1);
+  const int heads = is_q ? p.hq : p.hkv;
   const int half = p.rot >> 1;
 
-  int64_t slot = -1;
-  if (kCache) {
-    slot = p.slots[t];
+  // K and V of the cache write go to head h of the slot's page; a padding
+  // token's go nowhere
+  int64_t page_row = -1;
+  if (kCache && !is_q && live) {
+    const int64_t slot = p.slots[t];
     if (slot >= static_cast<int64_t>(p.num_blocks) * 16) {
-      if (threadIdx.x == 0 && blockIdx.y == 0) raise_error(p.err, PA_DEV_ERR_SLOT);
-      slot = -1;
+      if (at == 0) raise_error(p.err, PA_DEV_ERR_SLOT);
+    } else if (slot >= 0) {
+      page_row = ((slot >> 4) * p.hkv * 16 + (slot & 15)) * kLanes + lane;
     }
   }
-  auto source = [&](int r) -> const uint4* {
-    if (r < p.hq) return p.q + t * p.q_stride + r * kLanes + lane;
-    if (!kCache || r < p.hq + p.hkv) return p.k + t * p.k_stride + (r - p.hq) * kLanes + lane;
-    return p.v + t * p.v_stride + (r - p.hq - p.hkv) * kLanes + lane;
-  };
-  // Row r of the token goes to q_out, k_out or, in a pool, head g of its slot's
-  // page; nullptr: a padding token's K and V.
-  auto target = [&](int r) -> uint4* {
-    if (r < p.hq) return p.q_out + t * p.q_out_stride + r * kLanes + lane;
-    if (!kCache) return p.k_out + t * p.k_out_stride + (r - p.hq) * kLanes + lane;
-    if (slot < 0) return nullptr;
-    const bool is_k = r < p.hq + p.hkv;
-    const int g = r - p.hq - (is_k ? 0 : p.hkv);
-    const int64_t at = (((slot >> 4) * p.hkv + g) * 16 + (slot & 15)) * kLanes + lane;
-    return (is_k ? p.k_pool : p.v_pool) + at;
-  };
+  if (kCache && part == p.q_parts + 1) {  // V: the rows as they are
+    if (page_row < 0) return;
+    const uint4* src = p.v + t * p.v_stride + lane;
+    for (int h = first; h < heads; h += kRopeRows * step) {
+      uint4 x[kRopeRows];
+#pragma unroll
+      for (int u = 0; u < kRopeRows; ++u)
+        if (h + u * step < heads) x[u] = src[(h + u * step) * kLanes];
+#pragma unroll
+      for (int u = 0; u < kRopeRows; ++u)
+        if (h + u * step < heads)
+          p.v_pool[page_row + static_cast<int64_t>(h + u * step) * 16 * kLanes] = x[u];
+    }
+    return;
+  }
+
+  const uint4* src = (is_q ? p.q + t * p.q_stride : p.k + t * p.k_stride) + lane;
+  uint4* dst = is_q ? p.q_out + t * p.q_out_stride + lane
+               : !kCache ? p.k_out + t * p.k_out_stride + lane
+               : page_row >= 0 ? p.k_pool + page_row : nullptr;
+  const int64_t dst_step = kCache && !is_q ? 16 * kLanes : kLanes;
+  const uint4* weight = is_q ? p.q_weight : p.k_weight;
 
   // the first rows are on their way while cos and sin are computed
-  int r0 = blockIdx.y * kGroups + group;
-  uint4 raw[kRopeUnroll];
+  uint4 raw[kRopeRows];
+  auto load = [&](int h) {
 #pragma unroll
-  for (int u = 0; u < kRopeUnroll; ++u)
-    if (r0 + u * step < p.rows) raw[u] = *source(r0 + u * step);
-  if (threadIdx.x < half)
-    turn[threadIdx.x] = turn_of(p.positions[t], p.inv_freq[threadIdx.x], p.factor);
-  __syncthreads();
-
-  // This lane's cos and sin: eight pairs in the half layout (the sine's sign is
-  // that of the lane's half), four in the interleaved one; (1, 0) past rot.
-  constexpr int kPairs = kInterleaved ? 4 : 8;
-  float c[kPairs], s[kPairs];
+    for (int u = 0; u < kRopeRows; ++u)
+      if (h + u * step < heads) raw[u] = src[(h + u * step) * kLanes];
+  };
+  if (live) {
+    load(first);
+    if (at < half) turn[mine][at] = turn_of(p.positions[t], p.inv_freq[at], p.factor);
+  }
   const int e = lane * 8;
   const bool low = e < half;
   const bool rotated = e < p.rot;
   const int partner = rotated ? (low ? lane + half / 8 : lane - half / 8) : lane;
-#pragma unroll
-  for (int j = 0; j < kPairs; ++j) {
-    const int i = kInterleaved ? e / 2 + j : (low ? e : e - half) + j;
-    const float2 cs = rotated ? turn[i] : make_float2(1.f, 0.f);
-    c[j] = cs.x;
-    s[j] = kInterleaved || !low ? cs.y : -cs.y;
-  }
   const uint4 none = make_uint4(0, 0, 0, 0);
-  const uint4 wq = p.q_weight ? p.q_weight[lane] : none;
-  const uint4 wk = p.k_weight ? p.k_weight[lane] : none;
+  const uint4 w = weight ? weight[lane] : none;
+  const uint4 wp = weight ? weight[partner] : none;
+  __syncthreads();
+  if (!live) return;  // whole warps: none takes part in a shuffle below
 
-  // every lane of a warp takes the same number of turns (shuffles)
-  const int first = blockIdx.y * kGroups;
-  for (int base = first; base < p.rows; base += kRopeUnroll * step, r0 += kRopeUnroll * step) {
-    uint4 now[kRopeUnroll];
+  // A and B of this lane's dims; dims past rot go through with A = the weight
+  float2 A[4], B[4];
 #pragma unroll
-    for (int u = 0; u < kRopeUnroll; ++u) {
-      now[u] = raw[u];
-      const int next = r0 + (kRopeUnroll + u) * step;
-      if (next < p.rows) raw[u] = *source(next);
+  for (int j = 0; j < 4; ++j) {
+    const float2 ws = weight ? unpack2(word(w, j)) : make_float2(1.f, 1.f);
+    if (!rotated) {
+      A[j] = ws;
+      B[j] = make_float2(-0.f, -0.f);  // adding -0 keeps the sign of a zero
+    } else if (kInterleaved) {  // a pair of dims, one angle
+      const float2 cs = turn[mine][e / 2 + j];
+      A[j] = make_float2(cs.x * ws.x, cs.x * ws.y);
+      B[j] = make_float2(-cs.y * ws.y, cs.y * ws.x);
+    } else {  // two dims, two angles; the sine's sign is that of the lane's half
+      const float2 wo = weight ? unpack2(word(wp, j)) : make_float2(1.f, 1.f);
+      const int i = (low ? e : e - half) + 2 * j;
+      const float2 c0 = turn[mine][i], c1 = turn[mine][i + 1];
+      A[j] = make_float2(c0.x * ws.x, c1.x * ws.y);
+      B[j] = low ? make_float2(-c0.y * wo.x, -c1.y * wo.y) : make_float2(c0.y * wo.x, c1.y * wo.y);
     }
+  }
+  // every lane of a warp takes the same number of turns (shuffles)
+  for (int base = 0; lead + base < heads; base += kRopeRows * step) {
+    uint4 now[kRopeRows];
 #pragma unroll
-    for (int u = 0; u < kRopeUnroll; ++u) {
-      const int r = r0 + u * step;
-      const bool live = r < p.rows;
-      const bool is_q = r < p.hq;
-      const bool is_v = kCache && r >= p.hq + p.hkv;
-      float x[8];
-      unpack8(live ? now[u] : none, x);
-      if (p.q_weight || p.k_weight) {
-        float sum = 0.f;
+    for (int u = 0; u < kRopeRows; ++u) now[u] = raw[u];
+    load(first + base + kRopeRows * step);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum = fmaf(x[j], x[j], sum);
-#pragma unroll
-        for (int m = kLanes / 2; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-        if (is_q ? p.q_weight != nullptr : p.k_weight != nullptr) {
-          const float inv = rsqrtf(sum * (1.f / D) + p.eps);
-          float w[8];
-          unpack8(is_q ? wq : wk, w);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] *= inv * w[j];
-        }
-      }
-      float y[8];
-      if (kInterleaved) {
+    for (int u = 0; u < kRopeRows; ++u) {
+      if (lead + base + u * step >= heads) break;
+      const int h = first + base + u * step;
+      const uint4 x4 = h < heads ? now[u] : none;
+      float r = 1.f;
+      if (weight) {
+        float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          y[2 * j] = x[2 * j] * c[j] - x[2 * j + 1] * s[j];
-          y[2 * j + 1] = x[2 * j + 1] * c[j] + x[2 * j] * s[j];
+          const float2 x = unpack2(word(x4, j));
+          sum = __ffma2_rn(x, x, sum);
         }
-      } else {
+        float ss = sum.x + sum.y;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float other = __shfl_sync(0xffffffffu, x[j], partner, kLanes);
-          y[j] = x[j] * c[j % kPairs] + other * s[j % kPairs];
-        }
+        for (int m = kLanes / 2; m > 0; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+        r = rsqrtf(ss * (1.f / D) + p.eps);
       }
-      // dims past rot go through as they are: a product with 0 would turn an
-      // infinity into NaN
-      if (!rotated) {
+      uint32_t o[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = x[j];
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t own = word(x4, j);
+        uint32_t other = own;
+        if (kInterleaved)
+          other = __byte_perm(own, own, 0x1032);  // the pair's other dim
+        else
+          other = __shfl_sync(0xffffffffu, own, partner, kLanes);
+        const float2 x = unpack2(own);
+        // a product with 0 would turn an infinity past rot into NaN
+        const float2 xo = rotated ? unpack2(other) : make_float2(0.f, 0.f);
+        float2 y = __ffma2_rn(x, A[j], __fmul2_rn(xo, B[j]));
+        if (weight) y = __fmul2_rn(y, make_float2(r, r));
+        o[j] = pack2(y);
       }
-      uint4 o;
-      o.x = pack2(y[0], y[1]);
-      o.y = pack2(y[2], y[3]);
-      o.z = pack2(y[4], y[5]);
-      o.w = pack2(y[6], y[7]);
-      if (is_v) o = now[u];  // V's bits, untouched
-      if (live) {
-        uint4* dst = target(r);
-        if (dst) *dst = o;
-      }
+      if (h < heads && dst) dst[h * dst_step] = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
 }
 
 template <int D>
-void launch_rope(const RopeParams& p, bool interleaved, bool cache, dim3 grid, cudaStream_t st) {
+void launch_rope(const RopeParams& p, bool interleaved, bool cache, int grid, cudaStream_t st) {
   if (interleaved) {
     if (cache)
       rope_kernel<D, true, true><<<grid, kRopeThreads, 0, st>>>(p);
@@ -224,18 +239,22 @@ void launch_rope(const RopeParams& p, bool interleaved, bool cache, dim3 grid, c
   }
 }
 
-// A token's rows are split over CTAs while there are fewer CTAs than the device
-// holds at once, down to one row per lane group.
+// The q heads are split over CTAs while there are few of these, down to one row
+// per lane group.
 int run_rope(RopeParams& p, int head_dim, int layout, bool cache, int num_tokens, void* stream) {
-  p.rows = p.hq + (cache ? 2 : 1) * p.hkv;
-  const int groups = kRopeThreads / (head_dim / 8);
-  const int most = (p.rows + groups - 1) / groups;
-  const int64_t want = (static_cast<int64_t>(num_sms()) * 8 + num_tokens - 1) / num_tokens;
-  const dim3 grid(num_tokens, static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(want, most))));
+  p.num_tokens = num_tokens;
+  const int groups = kRopeTokenThreads / (head_dim / 8);
+  const int most = (p.hq + groups - 1) / groups;
+  const int blocks = (num_tokens + kRopeTokens - 1) / kRopeTokens;
+  const int want = num_sms() * kRopeCtasPerSm / blocks;
+  p.q_parts = std::max(1, std::min(want, most));
+  p.parts = p.q_parts + (p.hkv > 0 ? 1 : 0) + (cache ? 1 : 0);
+  const int64_t grid = static_cast<int64_t>(blocks) * p.parts;
+  if (grid > 0x7fffffff) return PA_ERR_UNSUPPORTED;
   if (head_dim == 128)
-    launch_rope<128>(p, layout == PA_ROPE_INTERLEAVED, cache, grid, as_stream(stream));
+    launch_rope<128>(p, layout == PA_ROPE_INTERLEAVED, cache, static_cast<int>(grid), as_stream(stream));
   else
-    launch_rope<64>(p, layout == PA_ROPE_INTERLEAVED, cache, grid, as_stream(stream));
+    launch_rope<64>(p, layout == PA_ROPE_INTERLEAVED, cache, static_cast<int>(grid), as_stream(stream));
   return launch_status();
 }
 
