@@ -23,6 +23,7 @@ __all__ = [
     "pa_chunked_prefill", "pa_gather_kv", "pa_get_device_error", "pa_sample", "pa_swap_blocks",
     "pa_read_probe",
     "pa_rope", "pa_rope_and_cache", "pa_rope_frequencies",
+    "pa_tree_attention", "pa_tree_workspace_size",
     "pool_desc", "lib",
     "PaError", "PA_KERNEL_AUTO", "PA_KERNEL_SIMT", "PA_KERNEL_TCGEN05",
     "PA_PREFILL_EXACT_WEIGHTS",
@@ -307,7 +308,7 @@ def pa_read_probe(k_pool, v_pool, block_tables, context_lens, num_ctas=None, out
 
 
 # ----------------------------------------------------------------------------
-# Drafting and eviction (include/pa_rope.h)
+# Drafting and eviction (include/pa_rope.h, include/pa_tree.h)
 #
 # These calls run on the device their tensors are on (whatever the current one)
 # and, without a `stream`, on that device's current stream; what they allocate
@@ -463,3 +464,65 @@ def pa_rope_and_cache(q, key, value, k_pool, v_pool, slot_mapping, positions, in
          int(bool(interleaved)), float(factor), k_pool.data_ptr(), v_pool.data_ptr(),
          desc, slot_mapping.data_ptr(), tokens)
     return q_out
+
+
+def _batch_args(k_pool, block_tables, context_lens, dev):
+    """Checks shared by the calls that read a batch's cache: ``(desc, S, max_blocks)``."""
+    torch = _torch()
+    _arg("k_pool", k_pool, torch.bfloat16, dev)
+    _dims("k_pool", k_pool, 4)
+    _arg("context_lens", context_lens, torch.int32, dev)
+    _dims("context_lens", context_lens, 1)
+    _arg("block_tables", block_tables, torch.int32, dev)
+    _dims("block_tables", block_tables, 2)
+    seqs, blocks = block_tables.shape
+    if context_lens.shape[0] != seqs:
+        raise ValueError(f"{seqs} block tables for {context_lens.shape[0]} context lengths")
+    return pool_desc(k_pool), seqs, blocks
+
+
+def pa_tree_workspace_size(max_q_len, num_q_heads, k_pool) -> int:
+    return int(_abi.load().pa_tree_workspace_size(int(max_q_len), int(num_q_heads),
+                                                  pool_desc(k_pool)))
+
+
+def pa_tree_attention(q, cu_q_lens, max_q_len, tree_mask, k_pool, v_pool, block_tables,
+                      context_lens, scale, out=None, lse=None, workspace=None, stream=None,
+                      want_lse=False):
+    """Attention of each sequence's drafted tokens (``q`` bf16 [total_q, Hq, D],
+    ``cu_q_lens`` int32 [S+1] on the device) over its cached tokens and, among the
+    drafted ones, those of the row's ``tree_mask`` (int64 [total_q, words], bit j of
+    word j // 64 = drafted token j).  ``context_lens`` counts the drafted tokens,
+    whose K and V are in the pools.  Returns ``(out, lse)``; ``lse`` is None unless
+    given or ``want_lse``."""
+    torch = _torch()
+    dev = q.device
+    qs = _rows_arg("q", q, dev)
+    total_q, hq, d = q.shape
+    desc, seqs, blocks = _batch_args(k_pool, block_tables, context_lens, dev)
+    if desc.head_dim != d:
+        raise ValueError(f"q has head_dim {d}, the pools {desc.head_dim}")
+    _arg("v_pool", v_pool, torch.bfloat16, dev, k_pool.shape)
+    _arg("cu_q_lens", cu_q_lens, torch.int32, dev, (seqs + 1,))
+    _arg("tree_mask", tree_mask, torch.int64, dev)
+    _dims("tree_mask", tree_mask, 2)
+    if tree_mask.shape[0] != total_q:
+        raise ValueError(f"tree_mask must have {total_q} rows, got {tree_mask.shape[0]}")
+    if out is None:
+        out = _empty((total_q, hq, d), torch.bfloat16, dev, stream)
+    else:
+        _arg("out", out, torch.bfloat16, dev, (total_q, hq, d))
+    if lse is not None:
+        _arg("lse", lse, torch.float32, dev, (total_q, hq))
+    elif want_lse:
+        lse = _empty((total_q, hq), torch.float32, dev, stream)
+    if workspace is None:
+        n = _abi.load().pa_tree_workspace_size(int(max_q_len), hq, desc)
+        workspace = _empty(max(n, 16), torch.uint8, dev, stream)
+    else:
+        _arg("workspace", workspace, torch.uint8, dev)
+    _run("pa_tree_attention", dev, stream, q.data_ptr(), qs, cu_q_lens.data_ptr(), total_q,
+         int(max_q_len), tree_mask.data_ptr(), tree_mask.shape[1], k_pool.data_ptr(),
+         v_pool.data_ptr(), desc, block_tables.data_ptr(), blocks, context_lens.data_ptr(), seqs,
+         hq, float(scale), out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel())
+    return out, lse

@@ -104,6 +104,11 @@ SIGNATURES = {
                                   c_vp, c_f32, c_vp, c_vp, c_i32, c_i32, c_f32, c_vp, c_vp,
                                   PoolDesc, c_vp, c_i32, c_vp]),
     "pa_rope_frequencies": (c_int, [c_i32, c_f64, c_i32, c_f64, c_f64, c_f64, c_f64, c_vp, c_vp]),
+    # attention of drafted trees (include/pa_tree.h)
+    "pa_tree_workspace_size": (c_size, [c_i32, c_i32, PoolDesc]),
+    "pa_tree_attention": (c_int, [c_vp, c_i64, c_vp, c_i32, c_i32, c_vp, c_i32, c_vp, c_vp,
+                                  PoolDesc, c_vp, c_i32, c_vp, c_i32, c_i32, c_f32, c_vp, c_vp,
+                                  c_vp, c_size, c_vp]),
     # paged read-bandwidth probe (include/pa_probe.h)
     "pa_read_probe": (c_int, [c_vp, c_vp, PoolDesc, c_vp, c_i32, c_vp, c_i32, c_vp, c_i32, c_vp]),
 }

@@ -1,0 +1,1025 @@
+// Attention of drafted trees over the paged cache, on the 5th-generation tensor
+// cores.
+//
+// The G = Hq/Hkv query heads of a sequence's n drafted tokens form rows (token,
+// head), token-major; floor(128/G) tokens make one 128-row tile, and an item is
+// (sequence, KV head, pass of up to two row tiles) over the sequence's key tiles
+// of 128.  Per row tile and key tile
+//     S [128 x 128] = Q . K^T            (D/16 MMAs)
+//     O [128 x D]  += P . V              (8 MMAs of P_hi, 8 of P_lo)
+// with fp32 accumulators in tensor memory; P = P_hi + P_lo, the weight with its
+// mantissa cut to bf16 and the same cut of the rest, replaces its scores in
+// tensor memory (per 32 keys: 16 columns of P_hi, 16 of P_lo) and is read there
+// by the second product.
+//
+// Two streams of (row tile, key tile) steps run side by side, each with its own
+// scores, accumulator and softmax warpgroup (a thread owns a row), so the tensor
+// cores work for one while the other's softmax runs:
+//   pair mode    (two row tiles): stream h takes row tile h, both take every key
+//                tile; K and V are read once for up to 256 rows.
+//   split mode   (one row tile): both take the same rows, stream h the key tiles
+//                h, h+2, ...; their results meet by log-sum-exp at the end.
+//
+// Work split: all items' key tiles, in order, are one line, and every CTA takes
+// an equal stretch of it (each finds its start from the lengths by a scan of its
+// own: no plan kernel, no queue).  An item inside one CTA's stretch is finished
+// there; one that crosses a border leaves normalised fp32 partial rows and
+// base-2 log-sum-exps in the workspace -- at most two items per CTA -- and a
+// second kernel, a programmatic dependent, merges them.
+//
+// Bound: HBM (K and V are read once per pass) up to about 256 rows of a KV head;
+// the tensor cores and the softmax warps beyond.
+//
+// Roles (one CTA per SM): warp 0 copies K and V pages (one ring, K and V of a
+// tile in turn), warp 1 issues the MMAs, warp 3 copies q and writes the border
+// descriptor, warps 4-7 and 8-11 are the two softmax warpgroups.  Every wait on
+// an mbarrier is bounded; the named barriers join warps that run the same steps
+// whatever happens.
+#include <math_constants.h>
+
+#include "../../include/pa_tree.h"
+#include "internal.h"
+#include "tc_common.cuh"
+
+namespace pa {
+namespace {
+
+using namespace tc;
+
+constexpr int kThreads = 384;
+constexpr int kMaxCtas = 160;      // partial results are sized for this many
+constexpr int kMinTiles = 2;       // key tiles of a stretch at least
+constexpr int kRegion = 128 * 128; // 128 rows x 128 bytes
+constexpr int kQSlots = 2;
+constexpr int kMaskRing = 16;
+constexpr float kRaiseLog2 = 16.f; // raise the maximum in use only past 2^16
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kOCol = 256;    // S_h at column 128 h, O_h at 256 + 128 h
+
+// Named barriers.
+constexpr int kBarMerge = 1;  // both warpgroups
+constexpr int kBarTail = 2;   // + h: one warpgroup; + 2: both
+
+template <int D>
+struct Cfg {
+  static constexpr int kHalves = D / 64;
+  static constexpr int kTileBytes = kHalves * kRegion;
+  static constexpr int kSlots = D == 128 ? 5 : 8;  // K/V ring
+  static constexpr int kPage = kHalves * 2048;     // bytes of a page
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffKV = kQSlots * kTileBytes;
+  static constexpr int kOffBar = kOffKV + kSlots * kTileBytes;
+  static constexpr int kNumBars = 2 * kQSlots + 2 * kSlots + 6 + 2;
+  static constexpr int kOffMisc = kOffBar + kNumBars * 8;
+  // tensor-memory slot, abort flag, plan {sequence, place in it (8 bytes)}
+  static constexpr int kOffMask = kOffMisc + 24;
+  static constexpr int kOffPoison = kOffMask + 4 * kMaskRing;  // [3 sets][2][4 words]
+  static constexpr int kOffX = (kOffPoison + 3 * 2 * 16 + 15) / 16 * 16;  // [128] (m, l)
+  static constexpr int kSmem = kOffX + 128 * 8 + 1024;
+  static_assert(kSmem <= 232448, "shared memory per CTA");
+};
+
+struct __align__(64) TreeParams {
+  CUtensorMap tm_k;
+  CUtensorMap tm_v;
+  CUtensorMap tm_q;
+  const int32_t* cu_q;
+  const uint32_t* mask;  // the int64 words as pairs of 32-bit ones
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  uint16_t* out;
+  float* lse;
+  int4* border;     // per CTA: the item that begins there and ends in a later CTA
+  float* part_lse;  // [2 * CTA + (begun there)][part_rows]
+  float* part_o;    // the same, [D]
+  unsigned int* err;
+  int total_q;
+  int max_n;        // drafted tokens of a sequence at most
+  int mask_words;   // 32-bit words of a mask row
+  int max_blocks;
+  int num_blocks;
+  int hkv;
+  int hq;
+  int group;
+  int tpt;          // tokens of a row tile
+  int num_seqs;
+  int part_rows;    // 128 or 256
+  float scale_log2;
+};
+
+// ---------------------------------------------------------------------------
+// Sequences, items and units
+// ---------------------------------------------------------------------------
+struct SeqRaw {
+  int q0, q1, L;
+};
+
+struct Seq {
+  int q0, n, L;
+  int tiles, passes;  // tiles 0: nothing to do
+};
+
+__device__ __forceinline__ int ld_i32(const int32_t* ptr) {
+  int x;
+  asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(x) : "l"(ptr));
+  return x;
+}
+
+__device__ __forceinline__ SeqRaw fetch_seq(const TreeParams& p, int s) {
+  SeqRaw r;
+  r.q0 = ld_i32(p.cu_q + s);
+  r.q1 = ld_i32(p.cu_q + s + 1);
+  r.L = ld_i32(p.context_lens + s);
+  return r;
+}
+
+__device__ __forceinline__ Seq decode_seq(const TreeParams& p, const SeqRaw& r, unsigned* err) {
+  Seq q;
+  q.q0 = r.q0;
+  q.n = r.q1 - r.q0;
+  q.L = r.L;
+  q.tiles = q.passes = 0;
+  const bool ok = r.q0 >= 0 && r.q1 >= r.q0 && r.q1 <= p.total_q && q.n <= p.max_n &&
+                  r.L >= q.n && r.L <= p.max_blocks * 16;
+  if (!ok && err) raise_error(err, PA_DEV_ERR_CONTEXT);
+  if (!ok || q.n == 0) return q;
+  q.tiles = (r.L + 127) >> 7;
+  q.passes = (q.n + 2 * p.tpt - 1) / (2 * p.tpt);
+  return q;
+}
+
+// A unit: one CTA's key tiles [tile0, tile0 + nt) of one item.
+struct Unit {
+  int s, g, rp, q0, n, L, c;
+  int i0;       // first token of the pass
+  int tile0, nt, tiles;
+  bool pair;    // two row tiles
+};
+
+// Walks a CTA's stretch of the line; every role has its own and all go the same
+// way.  The next sequence's values are loaded when a sequence is entered.
+struct Walk {
+  int s, g, rp, tile;
+  long long left;  // key tiles still to take
+  Seq cur;
+  SeqRaw next;
+
+  __device__ __forceinline__ void enter(const TreeParams& p, int s_, const SeqRaw& raw) {
+    s = s_;
+    cur = decode_seq(p, raw, nullptr);
+    if (s + 1 < p.num_seqs) next = fetch_seq(p, s + 1);
+  }
+  __device__ __forceinline__ void start(const TreeParams& p, int s0, long long at, long long count) {
+    left = count;
+    if (count <= 0) return;
+    enter(p, s0, fetch_seq(p, s0));
+    const long long item = at / cur.tiles;
+    tile = static_cast<int>(at - item * cur.tiles);
+    g = static_cast<int>(item / cur.passes);
+    rp = static_cast<int>(item % cur.passes);
+  }
+  __device__ __forceinline__ bool get(const TreeParams& p, Unit& u) {
+    if (left <= 0) return false;
+    u.s = s;
+    u.g = g;
+    u.rp = rp;
+    u.q0 = cur.q0;
+    u.n = cur.n;
+    u.L = cur.L;
+    u.c = cur.L - cur.n;
+    u.i0 = rp * 2 * p.tpt;
+    u.pair = cur.n - u.i0 > p.tpt;
+    u.tile0 = tile;
+    u.tiles = cur.tiles;
+    u.nt = left < cur.tiles - tile ? static_cast<int>(left) : cur.tiles - tile;
+    left -= u.nt;
+    tile += u.nt;
+    if (tile == cur.tiles) {
+      tile = 0;
+      if (++rp == cur.passes) {
+        rp = 0;
+        if (++g == p.hkv) {
+          g = 0;
+          while (left > 0 && s + 1 < p.num_seqs) {
+            enter(p, s + 1, next);
+            if (cur.tiles > 0) break;
+          }
+        }
+      }
+    }
+    return true;
+  }
+};
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  return static_cast<uint32_t>(f32_to_bf16_bits(lo)) |
+         (static_cast<uint32_t>(f32_to_bf16_bits(hi)) << 16);
+}
+
+// 32 keys' visibility for one row, from key c + rel on: cached ones (rel < 0) are
+// seen, drafted ones by the row's mask, ones past the context are not.
+__device__ __forceinline__ uint32_t mask_word(const uint32_t* row, int j, int n) {
+  if (j < 0) return 0xffffffffu;
+  const int have = n - 32 * j;
+  if (have <= 0) return 0;
+  const uint32_t w = __ldg(row + j);
+  return have >= 32 ? w : w & ((1u << have) - 1u);
+}
+__device__ __forceinline__ uint32_t visible32(const uint32_t* row, int rel, int n) {
+  const int j = rel >> 5;  // floor
+  return __funnelshift_r(mask_word(row, j, n), mask_word(row, j + 1, n), rel & 31);
+}
+
+__device__ __forceinline__ bool nonfinite_pair(uint32_t w) {
+  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+
+// ---------------------------------------------------------------------------
+// The kernel
+// ---------------------------------------------------------------------------
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_constant__ TreeParams p) {
+  using C = Cfg<D>;
+  constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, false, false);
+  constexpr uint32_t kIdescO = idesc_bf16_f32(128, D, false, true);
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sbase = (raw + 1023u) & ~1023u;
+  unsigned char* sptr = smem_raw + (sbase - raw);
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(sptr + C::kOffBar);
+  uint64_t* q_empty = q_full + kQSlots;
+  uint64_t* kv_full = q_empty + kQSlots;   // ring position 2t: K of tile t, 2t + 1: V
+  uint64_t* kv_empty = kv_full + C::kSlots;
+  uint64_t* s_full = kv_empty + C::kSlots;  // per stream: scores ready
+  uint64_t* p_full = s_full + 2;            // weights written back
+  uint64_t* pv_done = p_full + 2;           // P.V complete
+  uint64_t* o_free = pv_done + 2;           // both accumulators of a unit read out
+  uint64_t* drain = o_free + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sptr + C::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sptr + C::kOffMisc + 4);
+  volatile int* plan_seq = reinterpret_cast<volatile int*>(sptr + C::kOffMisc + 8);
+  volatile long long* plan_at = reinterpret_cast<volatile long long*>(sptr + C::kOffMisc + 16);
+  // loaded pages of key tile t, in slot t % kMaskRing
+  volatile uint32_t* kmask = reinterpret_cast<volatile uint32_t*>(sptr + C::kOffMask);
+  // drafted tokens of a tile whose V is not finite: [set: stream 0, stream 1,
+  // both][in turn][key / 32]
+  volatile uint32_t* poison_s = reinterpret_cast<volatile uint32_t*>(sptr + C::kOffPoison);
+  float2* xbuf = reinterpret_cast<float2*>(sptr + C::kOffX);
+  static_assert(C::kOffMisc % 8 == 0, "the plan's 8-byte word");
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < kQSlots; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
+    }
+    for (int i = 0; i < C::kSlots; ++i) {
+      mbar_init(&kv_full[i], 1);
+      mbar_init(&kv_empty[i], 1);
+    }
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(&s_full[h], 1);
+      mbar_init(&p_full[h], 4);  // one arrival per warp of the stream
+      mbar_init(&pv_done[h], 1);
+    }
+    mbar_init(o_free, 8);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    prefetch_tmap(&p.tm_k);
+    prefetch_tmap(&p.tm_v);
+    prefetch_tmap(&p.tm_q);
+  }
+  // the merge kernel may be set up now (it waits for this grid's end)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // Where this CTA's stretch begins.  Thread i sums a run of sequences, a scan
+  // over the threads places the runs on the line, and the thread whose run holds
+  // the CTA's first tile finds it there.
+  long long chunk, total;
+  {
+    __shared__ long long warp_sum[kThreads / 32];
+    const int per = (p.num_seqs + kThreads - 1) / kThreads;
+    const int s_lo = min(tid * per, p.num_seqs), s_hi = min(s_lo + per, p.num_seqs);
+    long long mine = 0;
+    for (int s = s_lo; s < s_hi; ++s) {
+      const Seq q = decode_seq(p, fetch_seq(p, s), blockIdx.x == 0 ? p.err : nullptr);
+      mine += static_cast<long long>(q.tiles) * q.passes * p.hkv;
+    }
+    long long scan = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, scan, o);
+      if (lane >= o) scan += v;
+    }
+    if (lane == 31) warp_sum[warp] = scan;
+    __syncthreads();
+    long long before = scan - mine;
+    total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += warp_sum[w];
+      total += warp_sum[w];
+    }
+    chunk = (total + gridDim.x - 1) / gridDim.x;
+    if (chunk < kMinTiles) chunk = kMinTiles;
+    const long long begin = chunk * blockIdx.x;
+    if (begin >= before && begin < before + mine) {
+      long long at = begin - before;
+      for (int s = s_lo; s < s_hi; ++s) {
+        const Seq q = decode_seq(p, fetch_seq(p, s), nullptr);
+        const long long cost = static_cast<long long>(q.tiles) * q.passes * p.hkv;
+        if (at < cost) {
+          *plan_seq = s;
+          *plan_at = at;
+          break;
+        }
+        at -= cost;
+      }
+    }
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, kTmemCols);
+  fence_barrier_init();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const long long begin = chunk * blockIdx.x;
+  const long long count = total - begin < chunk ? total - begin : chunk;
+  const int rows_box = p.tpt * p.group;
+  Walk walk;
+  walk.start(p, count > 0 ? *plan_seq : 0, count > 0 ? *plan_at : 0, count);
+  Unit u;
+
+  if (warp == 0) {
+    // ======================== K and V producer ========================
+    uint32_t pos = 0, kt = 0;
+    int slot = 0;
+    uint32_t phase = 0;
+    while (walk.get(p, u)) {
+      const int32_t* table = p.block_tables + static_cast<int64_t>(u.s) * p.max_blocks;
+      const int blocks = (u.L + 15) >> 4;
+      // block-table entries, four tiles at a time: this group's and the next's
+      auto entries = [&](int tile) {
+        const int b = tile * 8 + lane;
+        return b < blocks ? ld_i32(table + b) : -1;
+      };
+      int ent = entries(u.tile0), ent_next = entries(u.tile0 + 4);
+      for (int j = 0; j < u.nt; ++j, ++kt) {
+        if (j > 0 && (j & 3) == 0) {
+          ent = ent_next;
+          ent_next = entries(u.tile0 + j + 4);
+        }
+        int pb = __shfl_sync(0xffffffffu, ent, (j & 3) * 8 + (lane & 7));
+        const bool wanted = lane < 8 && (u.tile0 + j) * 8 + lane < blocks;
+        if (wanted && (pb < 0 || pb >= p.num_blocks)) {
+          raise_error(p.err, PA_DEV_ERR_BLOCK_ID);
+          pb = -1;
+        }
+        const bool get = wanted && pb >= 0;
+        const unsigned vm = __ballot_sync(0xffffffffu, get);
+        const int row = (pb * p.hkv + u.g) * 16;
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          mbar_wait(&kv_empty[slot], phase ^ 1, abort_flag, p.err);
+          if (!*abort_flag) {
+            if (lane == 0) {
+              if (v == 0) kmask[kt % kMaskRing] = vm;
+              mbar_arrive_expect_tx(&kv_full[slot], __popc(vm) * C::kPage);
+            }
+            __syncwarp();
+            if (get) {
+              const uint32_t dst = sbase + C::kOffKV + slot * C::kTileBytes;
+              if (v == 0) {  // K half by half, 128 rows each
+                tma_load_2d(dst + lane * 2048, &p.tm_k, 0, row, &kv_full[slot]);
+                if (D == 128)
+                  tma_load_2d(dst + kRegion + lane * 2048, &p.tm_k, 64, row, &kv_full[slot]);
+              } else {  // V page by page, its halves next to each other
+                if (D == 128)
+                  tma_load_3d(dst + lane * C::kPage, &p.tm_v, 0, row, 0, &kv_full[slot]);
+                else
+                  tma_load_2d(dst + lane * C::kPage, &p.tm_v, 0, row, &kv_full[slot]);
+              }
+            }
+            ++pos;
+          }
+          if (++slot == C::kSlots) {
+            slot = 0;
+            phase ^= 1;
+          }
+        }
+      }
+    }
+    if (*abort_flag && lane == 0)  // the copies in flight land before the CTA ends
+      for (uint32_t w = pos > C::kSlots ? pos - C::kSlots : 0; w < pos; ++w)
+        mbar_wait(&kv_full[w % C::kSlots], (w / C::kSlots) & 1, nullptr, p.err);
+  } else if (warp == 3) {
+    // ============== q producer, and the item that crosses out ==============
+    uint32_t qi = 0;
+    long long at = begin;
+    int4 border = make_int4(-1, 0, 0, 0);
+    while (walk.get(p, u)) {
+      const int tiles = u.pair ? 2 : 1;
+      for (int h = 0; h < tiles; ++h, ++qi) {
+        const int qs = qi % kQSlots;
+        mbar_wait(&q_empty[qs], ((qi / kQSlots) & 1) ^ 1, abort_flag, p.err);
+        if (*abort_flag) break;
+        if (lane == 0) {
+          const uint32_t dst = sbase + C::kOffQ + qs * C::kTileBytes;
+          const int token = u.q0 + u.i0 + h * p.tpt;
+          mbar_arrive_expect_tx(&q_full[qs], C::kHalves * rows_box * 128);
+          tma_load_3d(dst, &p.tm_q, 0, u.g * p.group, token, &q_full[qs]);
+          if (D == 128) tma_load_3d(dst + kRegion, &p.tm_q, 64, u.g * p.group, token, &q_full[qs]);
+        }
+        __syncwarp();
+      }
+      if (u.tile0 == 0 && u.nt < u.tiles)
+        border = make_int4(u.s, u.g, u.rp, static_cast<int>((at + u.tiles - 1) / chunk));
+      at += u.nt;
+    }
+    if (lane == 0) p.border[blockIdx.x] = border;
+    if (*abort_flag && lane == 0)
+      for (uint32_t w = qi > kQSlots ? qi - kQSlots : 0; w < qi; ++w)
+        mbar_wait(&q_full[w % kQSlots], (w / kQSlots) & 1, nullptr, p.err);
+  } else if (warp == 1) {
+    // ============================= MMA ==============================
+    // One lane issues the scores of the next step and the P.V of an earlier one,
+    // each as soon as its inputs are there (non-blocking polls, one limit on time
+    // without progress).  Steps are taken in the order (key tile, stream).
+    if (lane == 0) {
+      const uint64_t dq0 = smem_desc_sw128(sbase + C::kOffQ, 16, 1024);
+      const uint64_t dk0 = smem_desc_sw128(sbase + C::kOffKV, 16, 1024);
+      const uint64_t dv0 = smem_desc_sw128(sbase + C::kOffKV, 2048, 1024);
+      // steps whose scores are issued and whose P.V is not (two at most), oldest
+      // in the low byte: stream | first of its unit << 1 | last reader of its V
+      // slot << 2 | slot << 3 | slot phase << 6 | unit parity << 7
+      uint32_t fifo = 0;
+      int pending = 0;
+      uint32_t n_s[2] = {0, 0}, n_pv[2] = {0, 0};  // steps of each stream issued
+      uint32_t qi = 0, unit = 0;
+      int w = 0, steps = 0;
+      int k_slot = 0;
+      uint32_t k_phase = 0;  // K of the current tile in the ring
+      bool have = false, s_end = false;
+      long long last = clock64();
+      while (!*abort_flag) {
+        bool prog = false;
+        if (pending > 0) {
+          const int h = fifo & 1;
+          const bool first = (fifo >> 1) & 1;
+          const int slot = (fifo >> 3) & 7;
+          if (mbar_test_wait(&kv_full[slot], (fifo >> 6) & 1) &&
+              mbar_test_wait(&p_full[h], (h ? n_pv[1] : n_pv[0]) & 1) &&
+              (!first || mbar_test_wait(o_free, ((fifo >> 7) & 1) ^ 1))) {
+            tc_fence_after();
+            const uint64_t vb = desc_add(dv0, slot * C::kTileBytes);
+            const uint32_t sp = tmem + h * 128;
+            const uint32_t oc = tmem + kOCol + h * 128;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              umma_ts(oc, sp + 32 * (k >> 1) + 8 * (k & 1), desc_add(vb, k * C::kPage), kIdescO,
+                      first && k == 0 ? 0u : 1u);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              umma_ts(oc, sp + 32 * (k >> 1) + 8 * (k & 1) + 16, desc_add(vb, k * C::kPage),
+                      kIdescO, 1u);
+            umma_commit(&pv_done[h]);
+            if ((fifo >> 2) & 1) umma_commit(&kv_empty[slot]);
+            if (h)
+              ++n_pv[1];
+            else
+              ++n_pv[0];
+            fifo >>= 8;
+            --pending;
+            prog = true;
+          }
+        }
+        if (!have && !s_end) {
+          have = walk.get(p, u);
+          s_end = !have;
+          w = 0;
+          steps = u.pair ? 2 * u.nt : u.nt;
+          prog = true;
+        }
+        if (have) {
+          const int h = w & 1;
+          const uint32_t qq = u.pair ? qi + h : qi;
+          const int qs = qq % kQSlots;
+          const uint32_t mine = h ? n_s[1] : n_s[0];
+          // scores replace the weights of the stream's last step: its P.V is done
+          if (pending < 2 && mbar_test_wait(&kv_full[k_slot], k_phase) &&
+              mbar_test_wait(&pv_done[h], (mine & 1) ^ 1) &&
+              mbar_test_wait(&q_full[qs], (qq / kQSlots) & 1)) {
+            tc_fence_after();
+            const uint64_t qa = desc_add(dq0, qs * C::kTileBytes);
+            const uint64_t kb = desc_add(dk0, k_slot * C::kTileBytes);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t off = (k >> 2) * kRegion + (k & 3) * 32;
+              umma_ss(tmem + h * 128, desc_add(qa, off), desc_add(kb, off), kIdescS,
+                      k > 0 ? 1u : 0u);
+            }
+            umma_commit(&s_full[h]);
+            int v_slot = k_slot + 1;
+            uint32_t v_phase = k_phase;
+            if (v_slot == C::kSlots) {
+              v_slot = 0;
+              v_phase ^= 1;
+            }
+            const bool tile_end = !u.pair || h == 1;
+            const bool first = w < 2;
+            const uint32_t info = static_cast<uint32_t>(h) | (first ? 2u : 0u) |
+                                  (tile_end ? 4u : 0u) | (static_cast<uint32_t>(v_slot) << 3) |
+                                  (v_phase << 6) | ((unit & 1) << 7);
+            fifo |= info << (8 * pending);
+            ++pending;
+            if (h)
+              ++n_s[1];
+            else
+              ++n_s[0];
+            if (tile_end) {
+              umma_commit(&kv_empty[k_slot]);
+              k_slot = v_slot + 1;
+              k_phase = v_phase;
+              if (k_slot == C::kSlots) {
+                k_slot = 0;
+                k_phase ^= 1;
+              }
+            }
+            ++w;
+            // the unit's last use of this q tile
+            if (u.pair ? w >= steps - 1 : w == steps) umma_commit(&q_empty[qs]);
+            if (w == steps) {
+              qi += u.pair ? 2 : 1;
+              ++unit;
+              have = false;
+            }
+            prog = true;
+          }
+        }
+        if (s_end && pending == 0) break;
+        if (prog) {
+          last = clock64();
+        } else if (clock64() - last > kWaitLimitCycles) {
+          *abort_flag = 1;
+          raise_error(p.err, PA_DEV_ERR_TIMEOUT);
+        }
+      }
+      umma_commit(drain);
+      mbar_wait(drain, 0, nullptr, p.err);
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ============================ softmax ============================
+    const int h = (warp - 4) >> 2;
+    const int q4 = warp & 3;
+    const int r = q4 * 32 + lane;  // row of the tile, TMEM lane
+    const uint32_t lane_addr = static_cast<uint32_t>(q4 * 32) << 16;
+    const uint32_t scol = tmem + lane_addr + h * 128;
+    const uint32_t o_col[2] = {tmem + lane_addr + kOCol, tmem + lane_addr + kOCol + 128};
+    const int ti = r / p.group;  // token of this row within its tile
+    const int head = r - ti * p.group;
+    const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
+    const float2 neg1 = make_float2(-1.f, -1.f);
+    uint32_t cnt = 0;         // this stream's steps
+    uint32_t kt0 = 0;         // ring number of the unit's first tile
+    // Tail tiles so far: two records of them are in use in turn, so one is only
+    // written again when everybody has passed the other's barrier.
+    uint32_t split_tails = 0, pair_tails = 0;
+    while (walk.get(p, u)) {
+      const int i0 = u.i0 + (u.pair ? h * p.tpt : 0);
+      const bool row_ok = r < rows_box && i0 + ti < u.n;
+      const bool warp_ok = __any_sync(0xffffffffu, row_ok);
+      const uint32_t* mrow = p.mask + static_cast<int64_t>(u.q0 + i0 + ti) * p.mask_words;
+      const int steps = u.pair ? u.nt : (u.nt - h + 1) >> 1;
+      float m = -CUDART_INF_F, l = 0.f;
+      bool bad = false;  // this row sees a drafted token whose V is not finite
+      for (int k = 0; k < steps; ++k, ++cnt) {
+        const int tl = u.pair ? k : 2 * k + h;
+        const uint32_t kt = kt0 + tl;
+        const int kv0 = (u.tile0 + tl) * 128;
+        mbar_wait(&s_full[h], cnt & 1, abort_flag, p.err);
+        tc_fence_after();
+        const uint32_t vm = kmask[kt % kMaskRing];
+        // A tail tile holds drafted tokens or the context's end (the lengths alone
+        // say so: all warps take its barrier, or none).  Any other tile whose
+        // pages were all loaded is whole: every row sees every key.
+        const bool tail = kv0 + 128 > u.c;
+        const bool whole = !tail && vm == 0xffu;
+        uint32_t vis[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+        if (!whole) {
+          volatile uint32_t* pw =
+              poison_s + ((u.pair ? 4 : 2 * h) + ((u.pair ? pair_tails : split_tails) & 1)) * 4;
+          if (!u.pair || h == 0) {
+            // Thread r looks after key row r of V: zero past the context and in
+            // pages that were not loaded (their weights are 0, and 0 times what
+            // is there could be NaN), and zero, on record, where a drafted
+            // token's V is not finite (rows that do not see it have weight 0).
+            const int key = kv0 + r;
+            const uint32_t vpos = 2 * kt + 1;
+            const int vs = vpos % C::kSlots;
+            mbar_wait(&kv_full[vs], (vpos / C::kSlots) & 1, abort_flag, p.err);
+            const bool dead = key >= u.L || !((vm >> (r >> 4)) & 1u);
+            const uint32_t vrow = sbase + C::kOffKV + vs * C::kTileBytes + (r >> 4) * C::kPage +
+                                  (r & 15) * 128;
+            bool odd = false;
+            if (!dead && key >= u.c) {
+#pragma unroll 1
+              for (int half = 0; half < C::kHalves; ++half)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                  const uint4 x = lds128(vrow + half * 2048 + j * 16);
+                  odd |= nonfinite_pair(x.x) | nonfinite_pair(x.y) | nonfinite_pair(x.z) |
+                         nonfinite_pair(x.w);
+                }
+            }
+            if (dead || odd) {
+#pragma unroll 1
+              for (int half = 0; half < C::kHalves; ++half)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sts128_zero(vrow + half * 2048 + j * 16);
+              fence_proxy_async_smem();
+            }
+            const uint32_t word = __ballot_sync(0xffffffffu, odd);
+            if (tail && lane == 0) pw[q4] = word;
+          }
+          if (tail) {
+            named_bar_sync(u.pair ? kBarTail + 2 : kBarTail + h, u.pair ? 256 : 128);
+            if (u.pair)
+              ++pair_tails;
+            else
+              ++split_tails;
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t pages = (((vm >> (2 * j)) & 1u) ? 0x0000ffffu : 0u) |
+                                   (((vm >> (2 * j + 1)) & 1u) ? 0xffff0000u : 0u);
+            vis[j] = row_ok ? visible32(mrow, kv0 + 32 * j - u.c, u.n) & pages : 0u;
+            if (tail) bad |= (vis[j] & pw[j]) != 0;
+          }
+        }
+        if (warp_ok) {
+          // The tile's maximum (scaled); keys that are not seen count as -inf.
+          float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+          for (int j = 0; j < 4; j += 2) {
+            float x[64];
+            tmem_ld64(scol + 32 * j, x);
+#pragma unroll
+            for (int i = 0; i < 64; i += 2) {
+              const float2 y = __fmul2_rn(make_float2(x[i], x[i + 1]), sc2);
+              x[i] = y.x;
+              x[i + 1] = y.y;
+            }
+            if (!whole) {
+#pragma unroll
+              for (int i = 0; i < 64; ++i)
+                x[i] = ((vis[j + (i >> 5)] >> (i & 31)) & 1u) ? x[i] : -CUDART_INF_F;
+            }
+#pragma unroll
+            for (int i = 0; i < 64; ++i) mx[i & 3] = fmaxf(mx[i & 3], x[i]);
+          }
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          // The maximum in use is raised (and O_h and l rescaled) only when the
+          // tile's exceeds it by 2^16: weights up to that cannot overflow fp32
+          // sums, and the division by l makes the result exact either way.
+          const bool raise = m == -CUDART_INF_F ? top != -CUDART_INF_F : top > m + kRaiseLog2;
+          if (__any_sync(0xffffffffu, raise)) {
+            const float f = !raise ? 1.f : m == -CUDART_INF_F ? 0.f : exp2f(m - top);
+            if (raise) m = top;
+            l *= f;
+            if (k > 0) {  // the stream's last P.V is done: this step's scores came after it
+#pragma unroll 1
+              for (int cc = 0; cc < D / 16; ++cc) {
+                float ov[16];
+                tmem_ld16((h ? o_col[1] : o_col[0]) + cc * 16, ov);
+                uint32_t ow[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) ow[i] = __float_as_uint(ov[i] * f);
+                tmem_st16((h ? o_col[1] : o_col[0]) + cc * 16, ow);
+              }
+            }
+          }
+          // Weights, in place of the scores: per 32 keys 16 columns of P_hi and
+          // 16 of P_lo.
+          const float nm = m == -CUDART_INF_F ? 0.f : -m;
+          const float2 nm2 = make_float2(nm, nm);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float x[32];
+            tmem_ld32(scol + 32 * j, x);
+            uint32_t w[32];
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              float2 y = __ffma2_rn(make_float2(x[i], x[i + 1]), sc2, nm2);
+              if (!whole) {
+                y.x = ((vis[j] >> i) & 1u) ? y.x : -CUDART_INF_F;
+                y.y = ((vis[j] >> (i + 1)) & 1u) ? y.y : -CUDART_INF_F;
+              }
+              const float2 e = make_float2(exp2f(y.x), exp2f(y.y));
+              sum[(i >> 1) & 1] = __fadd2_rn(sum[(i >> 1) & 1], e);
+              const uint32_t ex = __float_as_uint(e.x), ey = __float_as_uint(e.y);
+              w[i >> 1] = __byte_perm(ex, ey, 0x7632);
+              const float2 hi = make_float2(__uint_as_float(ex & 0xffff0000u),
+                                            __uint_as_float(ey & 0xffff0000u));
+              const float2 lo = __ffma2_rn(hi, neg1, e);  // e - P_hi, exact
+              w[16 + (i >> 1)] = __byte_perm(__float_as_uint(lo.x), __float_as_uint(lo.y), 0x7632);
+            }
+            tmem_st32_nowait(scol + 32 * j, w);
+          }
+          tmem_wait_st();
+          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[h]);
+      }
+
+      // End of the unit: this row's output and log-sum-exp of the unit's keys.
+      if (steps > 0) mbar_wait(&pv_done[h], (cnt - 1) & 1, abort_flag, p.err);
+      float m0 = m, l0 = l, m1 = -CUDART_INF_F, l1 = 0.f;
+      if (!u.pair) {
+        // both streams hold a part of the same rows: (m, l) are exchanged in one
+        // buffer (l with its sign set where the row is bad)
+        const float2 own = make_float2(m, bad ? -l : l);
+        float2 other;
+        tc_fence_before();
+        if (h == 1) xbuf[r] = own;
+        named_bar_sync(kBarMerge, 256);
+        if (h == 0) {
+          other = xbuf[r];
+          xbuf[r] = own;
+        }
+        named_bar_sync(kBarMerge, 256);
+        if (h == 1) other = xbuf[r];
+        bad |= signbit(other.y);
+        m0 = h == 0 ? m : other.x;
+        l0 = h == 0 ? l : fabsf(other.y);
+        m1 = h == 0 ? other.x : m;
+        l1 = h == 0 ? fabsf(other.y) : l;
+      }
+      tc_fence_after();
+      const float M = fmaxf(m0, m1);
+      const float e0 = m0 == -CUDART_INF_F ? 0.f : exp2f(m0 - M);
+      const float e1 = m1 == -CUDART_INF_F ? 0.f : exp2f(m1 - M);
+      const float L = l0 * e0 + l1 * e1;
+      // l > 0, or NaN where a score was
+      const bool live = !(L == 0.f);
+      const float inv = bad ? CUDART_NAN_F : live ? 1.f / L : 0.f;
+      const float f0 = e0 * inv, f1 = e1 * inv;
+      const float lse2 = live ? M + log2f(L) : -CUDART_INF_F;
+      const bool full = u.nt == u.tiles;
+      const int64_t orow = static_cast<int64_t>(u.q0 + i0 + ti) * p.hq + u.g * p.group + head;
+      const int64_t prow = static_cast<int64_t>(2 * blockIdx.x + (u.tile0 == 0 ? 1 : 0)) *
+                               p.part_rows + (u.pair ? h * 128 : 0) + r;
+      // pair mode: all D dims of this stream's row; split mode: this warpgroup's
+      // half of the dims, from both accumulators
+      const int d0 = u.pair ? 0 : h * (D / 2);
+      const int dims = u.pair ? D : D / 2;
+      const uint32_t src = (u.pair ? (h ? o_col[1] : o_col[0]) : o_col[0]) + d0;
+      const bool two = !u.pair && u.nt > 1;  // stream 1 had a tile
+      if (warp_ok) {
+#pragma unroll 1
+        for (int cc = 0; cc < dims; cc += 32) {
+          float a[32];
+          tmem_ld32(src + cc, a);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) a[i] *= u.pair ? inv : f0;
+          if (two) {
+            float b[32];
+            tmem_ld32(src + 128 + cc, b);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) a[i] = fmaf(b[i], f1, a[i]);
+          }
+          // nothing seen: the accumulator of all-zero weights is zero, and stays so
+          if (row_ok && full) {
+            uint4* dst = reinterpret_cast<uint4*>(p.out + orow * D + d0 + cc);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              dst[i] = make_uint4(pack_bf16x2(a[8 * i], a[8 * i + 1]),
+                                  pack_bf16x2(a[8 * i + 2], a[8 * i + 3]),
+                                  pack_bf16x2(a[8 * i + 4], a[8 * i + 5]),
+                                  pack_bf16x2(a[8 * i + 6], a[8 * i + 7]));
+          } else if (row_ok) {
+            float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + d0 + cc);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              dst[i] = make_float4(a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(o_free);
+      if (row_ok && (u.pair || h == 0)) {
+        if (!full)
+          p.part_lse[prow] = lse2;
+        else if (p.lse)
+          p.lse[orow] = live ? lse2 * kLn2 : -CUDART_INF_F;
+      }
+      kt0 += u.nt;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Merge: block (c, y) takes rows of the item that begins in CTA c and ends in a
+// later one; a warp per row.  part i of the item is CTA c's "begun there" part
+// for i = 0 and CTA c + i's other part after that.
+// ---------------------------------------------------------------------------
+constexpr int kMergeWarps = 4;
+
+template <int D>
+__global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(
+    const __grid_constant__ TreeParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int4 b = p.border[blockIdx.x];
+  if (b.x < 0) return;
+  const int lane = threadIdx.x & 31;
+  const int q0 = p.cu_q[b.x], n = p.cu_q[b.x + 1] - q0;
+  const int parts = b.w - static_cast<int>(blockIdx.x) + 1;
+  constexpr int kPer = D / 32;  // dims of a lane
+  for (int row = blockIdx.y * kMergeWarps + (threadIdx.x >> 5); row < p.part_rows;
+       row += gridDim.y * kMergeWarps) {
+    const int h = row >> 7, r = row & 127;
+    const int ti = r / p.group, head = r - ti * p.group;
+    const int token = b.z * 2 * p.tpt + h * p.tpt + ti;
+    if (ti >= p.tpt || token >= n) continue;
+    auto at = [&](int i) {
+      const int64_t cta = blockIdx.x + i;
+      return (2 * cta + (i == 0 ? 1 : 0)) * p.part_rows + row;
+    };
+    float top = -CUDART_INF_F;
+    for (int i = lane; i < parts; i += 32) top = fmaxf(top, p.part_lse[at(i)]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float ref = top == -CUDART_INF_F ? 0.f : top;
+    float z = 0.f;
+    float acc[kPer];
+#pragma unroll
+    for (int d = 0; d < kPer; ++d) acc[d] = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < parts; ++i) {
+      const int64_t a = at(i);
+      const float w = exp2f(p.part_lse[a] - ref);  // 0 for an empty part
+      z += w;
+      const float* o = p.part_o + a * D + lane * kPer;
+#pragma unroll
+      for (int d = 0; d < kPer; ++d) acc[d] = fmaf(w, o[d], acc[d]);
+    }
+    const bool live = !(z == 0.f);
+    const float inv = live ? 1.f / z : 0.f;
+    const int64_t orow = static_cast<int64_t>(q0 + token) * p.hq + b.y * p.group + head;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + orow * D) + lane * (kPer / 2);
+#pragma unroll
+    for (int d = 0; d < kPer; d += 2) dst[d / 2] = pack_bf16x2(acc[d] * inv, acc[d + 1] * inv);
+    if (p.lse && lane == 0) p.lse[orow] = live ? (ref + log2f(z)) * kLn2 : -CUDART_INF_F;
+  }
+}
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+int rows_of(int max_q_len, int group) { return max_q_len > 128 / group ? 256 : 128; }
+
+template <int D>
+int launch_tree(TreeParams& p, const void* q, int64_t q_stride, const void* k_pool,
+                const void* v_pool, const pa_pool_desc& pool, int64_t most_tiles,
+                cudaStream_t stream) {
+  const int64_t rows = static_cast<int64_t>(pool.num_blocks) * pool.num_kv_heads * 16;
+  {
+    const uint64_t dims[2] = {static_cast<uint64_t>(D), static_cast<uint64_t>(rows)};
+    const uint64_t strides[1] = {D * 2};
+    const uint32_t box[2] = {64, 16};
+    if (!encode_bf16_map(&p.tm_k, k_pool, 2, dims, strides, box)) return PA_ERR_CUDA;
+    if (D == 64 && !encode_bf16_map(&p.tm_v, v_pool, 2, dims, strides, box)) return PA_ERR_CUDA;
+  }
+  if (D == 128) {
+    // V: (dim within a 64-dim half, pool row, half): one copy moves both halves
+    const uint64_t dims[3] = {64, static_cast<uint64_t>(rows), 2};
+    const uint64_t strides[2] = {D * 2, 128};
+    const uint32_t box[3] = {64, 16, 2};
+    if (!encode_bf16_map(&p.tm_v, v_pool, 3, dims, strides, box)) return PA_ERR_CUDA;
+  }
+  {
+    const uint64_t dims[3] = {static_cast<uint64_t>(D), static_cast<uint64_t>(p.hq),
+                              static_cast<uint64_t>(p.total_q)};
+    const uint64_t strides[2] = {D * 2, static_cast<uint64_t>(q_stride) * 2};
+    const uint32_t box[3] = {64, static_cast<uint32_t>(p.group), static_cast<uint32_t>(p.tpt)};
+    if (!encode_bf16_map(&p.tm_q, q, 3, dims, strides, box)) return PA_ERR_CUDA;
+  }
+  static KernelLaunchCache cache;
+  if (cache.blocks_per_sm(reinterpret_cast<const void*>(tree_tc_kernel<D>), kThreads,
+                          Cfg<D>::kSmem) < 1)
+    return PA_ERR_CUDA;
+  const int sms = num_sms() < kMaxCtas ? num_sms() : kMaxCtas;
+  const int grid = static_cast<int>(most_tiles < sms ? most_tiles : sms);
+  tree_tc_kernel<D><<<grid, kThreads, Cfg<D>::kSmem, stream>>>(p);
+  const int st = launch_status();
+  if (st != PA_OK) return st;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, p.part_rows / (2 * kMergeWarps));
+  cfg.blockDim = dim3(32 * kMergeWarps);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, tree_merge_kernel<D>, p) != cudaSuccess) {
+    cudaGetLastError();
+    return PA_ERR_CUDA;
+  }
+  return PA_OK;
+}
+
+}  // namespace
+}  // namespace pa
+
+using namespace pa;
+
+extern "C" {
+
+size_t pa_tree_workspace_size(int32_t max_q_len, int32_t num_q_heads, pa_pool_desc pool) {
+  if (max_q_len <= 0 || num_q_heads <= 0 || pool.num_kv_heads <= 0 || pool.head_dim <= 0 ||
+      num_q_heads < pool.num_kv_heads || num_q_heads / pool.num_kv_heads > 16)
+    return 0;
+  const size_t rows = size_t(2) * kMaxCtas * rows_of(max_q_len, num_q_heads / pool.num_kv_heads);
+  return align256(sizeof(int4) * kMaxCtas) + align256(sizeof(float) * rows) +
+         sizeof(float) * rows * pool.head_dim;
+}
+
+int pa_tree_attention(const void* q, int64_t q_stride, const int32_t* cu_q_lens, int32_t total_q,
+                      int32_t max_q_len, const int64_t* tree_mask, int32_t mask_words,
+                      const void* k_pool, const void* v_pool, pa_pool_desc pool,
+                      const int32_t* block_tables, int32_t max_blocks_per_seq,
+                      const int32_t* context_lens, int32_t num_seqs, int32_t num_q_heads,
+                      float scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                      void* stream) {
+  PA_NVTX_RANGE("pa_tree_attention");
+  const int st = check_pool(pool);
+  if (st != PA_OK) return st;
+  if (num_seqs < 0 || total_q < 0 || num_q_heads <= 0 || max_blocks_per_seq <= 0)
+    return PA_ERR_ARG;
+  if (num_q_heads % pool.num_kv_heads) return PA_ERR_SHAPE;
+  const int group = num_q_heads / pool.num_kv_heads;
+  if (group > 16) return PA_ERR_UNSUPPORTED;
+  if (num_seqs == 0 || total_q == 0) return PA_OK;
+  if (max_q_len < 1 || mask_words < 1 || static_cast<int64_t>(mask_words) * 64 < max_q_len)
+    return PA_ERR_ARG;
+  // the context limit keeps a sequence's positions, and a pool's rows, in an int
+  const int64_t rows = static_cast<int64_t>(pool.num_blocks) * pool.num_kv_heads * 16;
+  if (max_q_len > PA_TREE_MAX_TOKENS || mask_words > (1 << 20) || total_q >= (1 << 30) ||
+      rows >= (1LL << 31) || max_blocks_per_seq > (1 << 26))
+    return PA_ERR_UNSUPPORTED;
+  if (!q || !cu_q_lens || !tree_mask || !k_pool || !v_pool || !block_tables || !context_lens ||
+      !out)
+    return PA_ERR_ARG;
+  if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out))
+    return PA_ERR_ARG;
+  if (q_stride < static_cast<int64_t>(num_q_heads) * pool.head_dim || q_stride % 8)
+    return PA_ERR_ARG;
+  if (!workspace || !aligned16(workspace) ||
+      workspace_bytes < pa_tree_workspace_size(max_q_len, num_q_heads, pool))
+    return PA_ERR_WORKSPACE;
+  TreeParams p = {};
+  p.err = device_error_word();
+  if (!p.err) return PA_ERR_CUDA;
+  p.cu_q = cu_q_lens;
+  p.mask = reinterpret_cast<const uint32_t*>(tree_mask);
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.out = static_cast<uint16_t*>(out);
+  p.lse = lse;
+  p.total_q = total_q;
+  p.max_n = max_q_len;
+  p.mask_words = 2 * mask_words;
+  p.max_blocks = max_blocks_per_seq;
+  p.num_blocks = pool.num_blocks;
+  p.hkv = pool.num_kv_heads;
+  p.hq = num_q_heads;
+  p.group = group;
+  p.tpt = 128 / group;
+  p.num_seqs = num_seqs;
+  p.part_rows = rows_of(max_q_len, group);
+  p.scale_log2 = scale * kLog2e;
+  char* ws = static_cast<char*>(workspace);
+  p.border = reinterpret_cast<int4*>(ws);
+  ws += align256(sizeof(int4) * kMaxCtas);
+  p.part_lse = reinterpret_cast<float*>(ws);
+  ws += align256(sizeof(float) * 2 * kMaxCtas * p.part_rows);
+  p.part_o = reinterpret_cast<float*>(ws);
+  const int64_t passes = (max_q_len + 2 * p.tpt - 1) / (2 * p.tpt);
+  const int64_t tiles = (static_cast<int64_t>(max_blocks_per_seq) * 16 + 127) / 128;
+  const int64_t most = tiles > kMaxCtas ? kMaxCtas : tiles * passes * num_seqs * p.hkv;
+  if (pool.head_dim == 128)
+    return launch_tree<128>(p, q, q_stride, k_pool, v_pool, pool, most, as_stream(stream));
+  return launch_tree<64>(p, q, q_stride, k_pool, v_pool, pool, most, as_stream(stream));
+}
+
+}  // extern "C"

@@ -66,6 +66,33 @@ def test_rope_and_cache_refusals(lib):
     refuse(call, _abi.PA_ERR_UNSUPPORTED, rot=40)
 
 
+def test_tree_refusals(lib):
+    big = 1 << 40
+
+    def call(q=FAKE, qs=512, cu=FAKE, total=6, max_n=5, mask=FAKE, words=1, kp=FAKE, vp=FAKE,
+             desc=None, tables=FAKE, blocks=4, lens=FAKE, seqs=2, hq=4, out=FAKE, lse=None,
+             ws=FAKE, ws_bytes=big):
+        return lib.pa_tree_attention(q, qs, cu, total, max_n, mask, words, kp, vp, desc or pool(),
+                                     tables, blocks, lens, seqs, hq, 1.0, out, lse, ws, ws_bytes,
+                                     None)
+    assert call(seqs=0) == _abi.PA_OK and call(total=0) == _abi.PA_OK
+    for kw in (dict(q=None), dict(cu=None), dict(mask=None), dict(kp=None), dict(vp=None),
+               dict(tables=None), dict(lens=None), dict(out=None), dict(q=ODD), dict(out=ODD),
+               dict(qs=256), dict(qs=516), dict(max_n=0), dict(words=0), dict(max_n=65),
+               dict(seqs=-1), dict(total=-1), dict(blocks=0), dict(hq=0)):
+        refuse(call, _abi.PA_ERR_ARG, **kw)
+    refuse(call, _abi.PA_ERR_SHAPE, hq=3)
+    for kw in (dict(hq=34, qs=34 * 128), dict(desc=pool(d=96)), dict(max_n=4097, words=65),
+               dict(desc=pool(nb=1 << 27))):
+        refuse(call, _abi.PA_ERR_UNSUPPORTED, **kw)
+    need = lib.pa_tree_workspace_size(5, 4, pool())
+    for kw in (dict(ws=None), dict(ws=ODD), dict(ws_bytes=need - 1), dict(ws_bytes=0)):
+        refuse(call, _abi.PA_ERR_WORKSPACE, **kw)
+    assert lib.pa_tree_workspace_size(200, 4, pool()) > need > 0
+    for bad in ((0, 4, pool()), (5, 0, pool()), (5, 1, pool()), (5, 40, pool())):
+        assert lib.pa_tree_workspace_size(*bad) == 0
+
+
 def test_frequencies():
     f, factor = pa.pa_rope_frequencies(8)
     assert factor == 1.0 and np.allclose(f, [1, 0.1, 0.01, 0.001], rtol=1e-15)
