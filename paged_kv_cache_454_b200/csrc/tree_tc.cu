@@ -13,28 +13,35 @@
 // by the second product.
 //
 // Two streams of (row tile, key tile) steps run side by side, each with its own
-// scores, accumulator and softmax warpgroup (a thread owns a row), so the tensor
-// cores work for one while the other's softmax runs:
+// scores, accumulator and two softmax warpgroups (a thread owns 64 keys of a
+// row), so the tensor cores work for one while the other's softmax runs:
 //   pair mode    (two row tiles): stream h takes row tile h, both take every key
 //                tile; K and V are read once for up to 256 rows.
 //   split mode   (one row tile): both take the same rows, stream h the key tiles
 //                h, h+2, ...; their results meet by log-sum-exp at the end.
+// The maximum that a row's weights are formed with is the same in both halves of
+// the row and stays until a tile's maximum exceeds it by 2^16 in some row of the
+// stream: one vote per step (an OR-reducing barrier); only then the halves
+// exchange maxima and the accumulator is rescaled.
 //
-// Work split: all items' key tiles, in order, are one line, and every CTA takes
-// an equal stretch of it (each finds its start from the lengths by a scan of its
-// own: no plan kernel, no queue).  An item inside one CTA's stretch is finished
-// there; one that crosses a border leaves normalised fp32 partial rows and
-// base-2 log-sum-exps in the workspace -- at most two items per CTA -- and a
-// second kernel, a programmatic dependent, merges them.
+// Work split: all items' key tiles, in order, are one line, with kItemCost more
+// places in front of every item for what it costs besides its tiles, and every
+// CTA takes an equal stretch of it (each finds its start from the lengths by a
+// scan of its own: no plan kernel, no queue).  An item inside one CTA's stretch
+// is finished there; one that crosses a border leaves normalised fp32 partial
+// rows and base-2 log-sum-exps in the workspace -- at most two items per CTA --
+// and a second kernel, a programmatic dependent, merges them.
 //
-// Bound: HBM (K and V are read once per pass) up to about 256 rows of a KV head;
+// Bound: HBM (K and V are read once per pass) up to about 128 rows of a KV head;
 // the tensor cores and the softmax warps beyond.
 //
 // Roles (one CTA per SM): warp 0 copies K and V pages (one ring, K and V of a
-// tile in turn), warp 1 issues the MMAs, warp 3 copies q and writes the border
-// descriptor, warps 4-7 and 8-11 are the two softmax warpgroups.  Every wait on
-// an mbarrier is bounded; the named barriers join warps that run the same steps
-// whatever happens.
+// tile in turn), warp 1 issues the MMAs, warp 2 walks the stretch and publishes
+// its units in a ring, warp 3 copies q, warps 4-19 are the softmax warpgroups
+// (stream, key half).  Every wait on an mbarrier is bounded.  The named barriers
+// join softmax warps that go through the same units and steps whatever happens:
+// after a time-out the data waits return at once and the unit ring, which depends
+// on nothing else, still runs to its end.
 #include <math_constants.h>
 
 #include "../../include/pa_tree.h"
@@ -46,19 +53,22 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 640;
 constexpr int kMaxCtas = 160;      // partial results are sized for this many
-constexpr int kMinTiles = 2;       // key tiles of a stretch at least
+constexpr int kMinPlaces = 2;      // places of a stretch at least
+constexpr int kItemCost = 2;       // places in front of an item
 constexpr int kRegion = 128 * 128; // 128 rows x 128 bytes
 constexpr int kQSlots = 2;
+constexpr int kUnits = 4;          // ring of units
+constexpr int kUnitReaders = 3 + 16;  // K/V, q, MMA, softmax warps
 constexpr int kMaskRing = 16;
 constexpr float kRaiseLog2 = 16.f; // raise the maximum in use only past 2^16
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOCol = 256;    // S_h at column 128 h, O_h at 256 + 128 h
 
 // Named barriers.
-constexpr int kBarMerge = 1;  // both warpgroups
-constexpr int kBarTail = 2;   // + h: one warpgroup; + 2: both
+constexpr int kBarBoth = 1;    // all softmax warps
+constexpr int kBarStream = 2;  // + h: the warps of one stream
 
 template <int D>
 struct Cfg {
@@ -68,14 +78,16 @@ struct Cfg {
   static constexpr int kPage = kHalves * 2048;     // bytes of a page
   static constexpr int kOffQ = 0;
   static constexpr int kOffKV = kQSlots * kTileBytes;
-  static constexpr int kOffBar = kOffKV + kSlots * kTileBytes;
-  static constexpr int kNumBars = 2 * kQSlots + 2 * kSlots + 6 + 2;
-  static constexpr int kOffMisc = kOffBar + kNumBars * 8;
+  static constexpr int kOffUnit = kOffKV + kSlots * kTileBytes;  // [kUnits] x 48 bytes
+  static constexpr int kOffX = kOffUnit + kUnits * 48;  // [4][128] floats: exchanges of a row
+  static constexpr int kOffBar = kOffX + 4 * 128 * 4;
+  static constexpr int kNumBars = 2 * kQSlots + 2 * kSlots + 2 * kUnits + 6 + 2;
   // tensor-memory slot, abort flag, plan {sequence, place in it (8 bytes)}
+  static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kOffMask = kOffMisc + 24;
-  static constexpr int kOffPoison = kOffMask + 4 * kMaskRing;  // [3 sets][2][4 words]
-  static constexpr int kOffX = (kOffPoison + 3 * 2 * 16 + 15) / 16 * 16;  // [128] (m, l)
-  static constexpr int kSmem = kOffX + 128 * 8 + 1024;
+  static constexpr int kOffPoison = kOffMask + 4 * kMaskRing;  // [3 sets][2][2 halves][4 words]
+  static constexpr int kSmem = kOffPoison + 3 * 2 * 2 * 16;
+  // kWarpSums of the start-up scan use the exchange buffer
   static_assert(kSmem <= 232448, "shared memory per CTA");
 };
 
@@ -148,67 +160,25 @@ __device__ __forceinline__ Seq decode_seq(const TreeParams& p, const SeqRaw& r, 
   return q;
 }
 
-// A unit: one CTA's key tiles [tile0, tile0 + nt) of one item.
+// Places of an item on the line, and of a sequence.
+__device__ __forceinline__ int item_places(const Seq& q) { return q.tiles + kItemCost; }
+__device__ __forceinline__ long long seq_places(const Seq& q, int hkv) {
+  return q.tiles ? static_cast<long long>(item_places(q)) * q.passes * hkv : 0;
+}
+
+// A unit: one CTA's key tiles [tile0, tile0 + nt) of one item; nt 0: no more.
+struct __align__(16) UnitWords {
+  int s, g, rp, q0;
+  int n, L, tile0, nt;
+  int tiles, pad0, pad1, pad2;
+};
+static_assert(sizeof(UnitWords) == 48, "three 16-byte words");
+
 struct Unit {
   int s, g, rp, q0, n, L, c;
   int i0;       // first token of the pass
   int tile0, nt, tiles;
   bool pair;    // two row tiles
-};
-
-// Walks a CTA's stretch of the line; every role has its own and all go the same
-// way.  The next sequence's values are loaded when a sequence is entered.
-struct Walk {
-  int s, g, rp, tile;
-  long long left;  // key tiles still to take
-  Seq cur;
-  SeqRaw next;
-
-  __device__ __forceinline__ void enter(const TreeParams& p, int s_, const SeqRaw& raw) {
-    s = s_;
-    cur = decode_seq(p, raw, nullptr);
-    if (s + 1 < p.num_seqs) next = fetch_seq(p, s + 1);
-  }
-  __device__ __forceinline__ void start(const TreeParams& p, int s0, long long at, long long count) {
-    left = count;
-    if (count <= 0) return;
-    enter(p, s0, fetch_seq(p, s0));
-    const long long item = at / cur.tiles;
-    tile = static_cast<int>(at - item * cur.tiles);
-    g = static_cast<int>(item / cur.passes);
-    rp = static_cast<int>(item % cur.passes);
-  }
-  __device__ __forceinline__ bool get(const TreeParams& p, Unit& u) {
-    if (left <= 0) return false;
-    u.s = s;
-    u.g = g;
-    u.rp = rp;
-    u.q0 = cur.q0;
-    u.n = cur.n;
-    u.L = cur.L;
-    u.c = cur.L - cur.n;
-    u.i0 = rp * 2 * p.tpt;
-    u.pair = cur.n - u.i0 > p.tpt;
-    u.tile0 = tile;
-    u.tiles = cur.tiles;
-    u.nt = left < cur.tiles - tile ? static_cast<int>(left) : cur.tiles - tile;
-    left -= u.nt;
-    tile += u.nt;
-    if (tile == cur.tiles) {
-      tile = 0;
-      if (++rp == cur.passes) {
-        rp = 0;
-        if (++g == p.hkv) {
-          g = 0;
-          while (left > 0 && s + 1 < p.num_seqs) {
-            enter(p, s + 1, next);
-            if (cur.tiles > 0) break;
-          }
-        }
-      }
-    }
-    return true;
-  }
 };
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
@@ -217,17 +187,39 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 }
 
 // 32 keys' visibility for one row, from key c + rel on: cached ones (rel < 0) are
-// seen, drafted ones by the row's mask, ones past the context are not.
-__device__ __forceinline__ uint32_t mask_word(const uint32_t* row, int j, int n) {
+// seen, drafted ones by the row's mask (its first two words are at hand), ones
+// past the context are not.
+__device__ __forceinline__ uint32_t mask_word(const uint32_t* row, uint2 head, int j, int n) {
   if (j < 0) return 0xffffffffu;
   const int have = n - 32 * j;
   if (have <= 0) return 0;
-  const uint32_t w = __ldg(row + j);
+  const uint32_t w = j == 0 ? head.x : j == 1 ? head.y : __ldg(row + j);
   return have >= 32 ? w : w & ((1u << have) - 1u);
 }
-__device__ __forceinline__ uint32_t visible32(const uint32_t* row, int rel, int n) {
+__device__ __forceinline__ uint32_t visible32(const uint32_t* row, uint2 head, int rel, int n) {
   const int j = rel >> 5;  // floor
-  return __funnelshift_r(mask_word(row, j, n), mask_word(row, j + 1, n), rel & 31);
+  return __funnelshift_r(mask_word(row, head, j, n), mask_word(row, head, j + 1, n), rel & 31);
+}
+
+// A wait of the unit ring: several times as long as the waits for data.
+__device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity, unsigned* err) {
+  for (int i = 0; i < 8; ++i)
+    if (mbar_wait(bar, parity, nullptr, err)) return true;
+  return false;
+}
+
+// OR of `pred` over the `count` threads of a named barrier.
+__device__ __forceinline__ bool barrier_any(int id, int count, bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred q, a;\n\t"
+      "setp.ne.u32 q, %1, 0;\n\t"
+      "bar.red.or.pred a, %2, %3, q;\n\t"
+      "selp.u32 %0, 1, 0, a;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(pred)), "r"(id), "r"(count)
+      : "memory");
+  return r != 0;
 }
 
 __device__ __forceinline__ bool nonfinite_pair(uint32_t w) {
@@ -242,32 +234,40 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
   using C = Cfg<D>;
   constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, false, false);
   constexpr uint32_t kIdescO = idesc_bf16_f32(128, D, false, true);
-  extern __shared__ unsigned char smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw);
-  const uint32_t sbase = (raw + 1023u) & ~1023u;
-  unsigned char* sptr = smem_raw + (sbase - raw);
-  uint64_t* q_full = reinterpret_cast<uint64_t*>(sptr + C::kOffBar);
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const uint32_t sbase = smem_u32(smem);
+  UnitWords* units = reinterpret_cast<UnitWords*>(smem + C::kOffUnit);
+  float* xbuf = reinterpret_cast<float*>(smem + C::kOffX);
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint64_t* q_empty = q_full + kQSlots;
   uint64_t* kv_full = q_empty + kQSlots;   // ring position 2t: K of tile t, 2t + 1: V
   uint64_t* kv_empty = kv_full + C::kSlots;
-  uint64_t* s_full = kv_empty + C::kSlots;  // per stream: scores ready
-  uint64_t* p_full = s_full + 2;            // weights written back
-  uint64_t* pv_done = p_full + 2;           // P.V complete
-  uint64_t* o_free = pv_done + 2;           // both accumulators of a unit read out
+  uint64_t* u_full = kv_empty + C::kSlots;
+  uint64_t* u_empty = u_full + kUnits;
+  uint64_t* s_full = u_empty + kUnits;  // per stream: scores ready
+  uint64_t* p_full = s_full + 2;        // weights written back
+  uint64_t* pv_done = p_full + 2;       // P.V complete
+  uint64_t* o_free = pv_done + 2;       // both accumulators of a unit read out
   uint64_t* drain = o_free + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sptr + C::kOffMisc);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(sptr + C::kOffMisc + 4);
-  volatile int* plan_seq = reinterpret_cast<volatile int*>(sptr + C::kOffMisc + 8);
-  volatile long long* plan_at = reinterpret_cast<volatile long long*>(sptr + C::kOffMisc + 16);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+  volatile int* plan_seq = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8);
+  volatile long long* plan_at = reinterpret_cast<volatile long long*>(smem + C::kOffMisc + 16);
   // loaded pages of key tile t, in slot t % kMaskRing
-  volatile uint32_t* kmask = reinterpret_cast<volatile uint32_t*>(sptr + C::kOffMask);
+  volatile uint32_t* kmask = reinterpret_cast<volatile uint32_t*>(smem + C::kOffMask);
   // drafted tokens of a tile whose V is not finite: [set: stream 0, stream 1,
-  // both][in turn][key / 32]
-  volatile uint32_t* poison_s = reinterpret_cast<volatile uint32_t*>(sptr + C::kOffPoison);
-  float2* xbuf = reinterpret_cast<float2*>(sptr + C::kOffX);
-  static_assert(C::kOffMisc % 8 == 0, "the plan's 8-byte word");
+  // both][in turn][64-dim half][key / 32]
+  volatile uint32_t* poison_s = reinterpret_cast<volatile uint32_t*>(smem + C::kOffPoison);
+  static_assert(C::kOffUnit % 16 == 0 && C::kOffMisc % 8 == 0, "alignment of the words");
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (sbase & 1023u) {  // the swizzled tiles need it, and the compiler gives it
+    if (tid == 0) {
+      raise_error(p.err, PA_DEV_ERR_TIMEOUT);
+      p.border[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    }
+    return;
+  }
   if (tid == 0) {
     for (int i = 0; i < kQSlots; ++i) {
       mbar_init(&q_full[i], 1);
@@ -277,12 +277,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
       mbar_init(&kv_full[i], 1);
       mbar_init(&kv_empty[i], 1);
     }
+    for (int i = 0; i < kUnits; ++i) {
+      mbar_init(&u_full[i], 1);
+      mbar_init(&u_empty[i], kUnitReaders);
+    }
     for (int h = 0; h < 2; ++h) {
       mbar_init(&s_full[h], 1);
-      mbar_init(&p_full[h], 4);  // one arrival per warp of the stream
+      mbar_init(&p_full[h], 8);  // one arrival per warp of the stream
       mbar_init(&pv_done[h], 1);
     }
-    mbar_init(o_free, 8);
+    mbar_init(o_free, 16);
     mbar_init(drain, 1);
     *abort_flag = 0;
     prefetch_tmap(&p.tm_k);
@@ -294,17 +298,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
 
   // Where this CTA's stretch begins.  Thread i sums a run of sequences, a scan
   // over the threads places the runs on the line, and the thread whose run holds
-  // the CTA's first tile finds it there.
+  // the CTA's first place finds it there.
   long long chunk, total;
   {
-    __shared__ long long warp_sum[kThreads / 32];
+    long long* warp_sum = reinterpret_cast<long long*>(xbuf);
     const int per = (p.num_seqs + kThreads - 1) / kThreads;
     const int s_lo = min(tid * per, p.num_seqs), s_hi = min(s_lo + per, p.num_seqs);
     long long mine = 0;
-    for (int s = s_lo; s < s_hi; ++s) {
-      const Seq q = decode_seq(p, fetch_seq(p, s), blockIdx.x == 0 ? p.err : nullptr);
-      mine += static_cast<long long>(q.tiles) * q.passes * p.hkv;
-    }
+    for (int s = s_lo; s < s_hi; ++s)
+      mine += seq_places(decode_seq(p, fetch_seq(p, s), blockIdx.x == 0 ? p.err : nullptr), p.hkv);
     long long scan = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -320,19 +322,18 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
       total += warp_sum[w];
     }
     chunk = (total + gridDim.x - 1) / gridDim.x;
-    if (chunk < kMinTiles) chunk = kMinTiles;
+    if (chunk < kMinPlaces) chunk = kMinPlaces;
     const long long begin = chunk * blockIdx.x;
     if (begin >= before && begin < before + mine) {
       long long at = begin - before;
       for (int s = s_lo; s < s_hi; ++s) {
-        const Seq q = decode_seq(p, fetch_seq(p, s), nullptr);
-        const long long cost = static_cast<long long>(q.tiles) * q.passes * p.hkv;
-        if (at < cost) {
+        const long long places = seq_places(decode_seq(p, fetch_seq(p, s), nullptr), p.hkv);
+        if (at < places) {
           *plan_seq = s;
           *plan_at = at;
           break;
         }
-        at -= cost;
+        at -= places;
       }
     }
   }
@@ -342,19 +343,112 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const long long begin = chunk * blockIdx.x;
-  const long long count = total - begin < chunk ? total - begin : chunk;
   const int rows_box = p.tpt * p.group;
-  Walk walk;
-  walk.start(p, count > 0 ? *plan_seq : 0, count > 0 ? *plan_at : 0, count);
-  Unit u;
 
-  if (warp == 0) {
+  // The next unit of the ring, for a whole warp (or the MMA's lane).  Its waits do
+  // not heed the abort flag (every role takes every unit) and outlast those that
+  // set it.
+  uint32_t u_at = 0;
+  Unit u;
+  auto next_unit = [&](bool whole_warp) -> bool {
+    const int slot = u_at % kUnits;
+    if (!ring_wait(&u_full[slot], (u_at / kUnits) & 1, p.err)) return false;
+    const int4* src = reinterpret_cast<const int4*>(&units[slot]);
+    const int4 a = src[0], b = src[1];
+    u.s = a.x;
+    u.g = a.y;
+    u.rp = a.z;
+    u.q0 = a.w;
+    u.n = b.x;
+    u.L = b.y;
+    u.tile0 = b.z;
+    u.nt = b.w;
+    u.tiles = units[slot].tiles;
+    u.c = u.L - u.n;
+    u.i0 = u.rp * 2 * p.tpt;
+    u.pair = u.n - u.i0 > p.tpt;
+    if (whole_warp) __syncwarp();
+    if (!whole_warp || lane == 0) mbar_arrive(&u_empty[slot]);
+    ++u_at;
+    return u.nt > 0;
+  };
+
+  if (warp == 2) {
+    // ============ the walk along the stretch, and its border ============
+    const long long begin = chunk * blockIdx.x;
+    long long left = total - begin < chunk ? total - begin : chunk;  // places still to take
+    long long at = begin;
+    int4 border = make_int4(-1, 0, 0, 0);
+    int s = 0, g = 0, rp = 0, place = 0;
+    Seq cur = {};
+    SeqRaw next = {};
+    auto enter = [&](const SeqRaw& r) {
+      cur = decode_seq(p, r, nullptr);
+      if (s + 1 < p.num_seqs) next = fetch_seq(p, s + 1);
+    };
+    if (left > 0) {
+      s = *plan_seq;
+      enter(fetch_seq(p, s));
+      const long long in = *plan_at;
+      const long long item = in / item_places(cur);
+      place = static_cast<int>(in - item * item_places(cur));
+      g = static_cast<int>(item / cur.passes);
+      rp = static_cast<int>(item % cur.passes);
+    }
+    while (true) {
+      UnitWords w = {};
+      while (left > 0) {  // the next stretch of places with a key tile among them
+        const int all = item_places(cur);
+        const int take = left < all - place ? static_cast<int>(left) : all - place;
+        const int t0 = max(0, place - kItemCost), t1 = max(0, place + take - kItemCost);
+        w.s = s;
+        w.g = g;
+        w.rp = rp;
+        w.q0 = cur.q0;
+        w.n = cur.n;
+        w.L = cur.L;
+        w.tile0 = t0;
+        w.nt = t1 - t0;
+        w.tiles = cur.tiles;
+        if (t0 == 0 && t1 > 0 && t1 < cur.tiles)  // ends in a later CTA
+          border = make_int4(s, g, rp, static_cast<int>((at - place + all - 1) / chunk));
+        left -= take;
+        at += take;
+        place += take;
+        if (place == all) {
+          place = 0;
+          if (++rp == cur.passes) {
+            rp = 0;
+            if (++g == p.hkv) {
+              g = 0;
+              while (left > 0 && s + 1 < p.num_seqs) {
+                const SeqRaw r = next;
+                ++s;
+                enter(r);
+                if (cur.tiles > 0) break;
+              }
+            }
+          }
+        }
+        if (w.nt > 0) break;
+      }
+      const int slot = u_at % kUnits;
+      if (!ring_wait(&u_empty[slot], ((u_at / kUnits) & 1) ^ 1, p.err)) break;
+      if (lane == 0) {
+        units[slot] = w;
+        mbar_arrive(&u_full[slot]);
+      }
+      __syncwarp();
+      ++u_at;
+      if (w.nt == 0) break;
+    }
+    if (lane == 0) p.border[blockIdx.x] = border;
+  } else if (warp == 0) {
     // ======================== K and V producer ========================
     uint32_t pos = 0, kt = 0;
     int slot = 0;
     uint32_t phase = 0;
-    while (walk.get(p, u)) {
+    while (next_unit(true)) {
       const int32_t* table = p.block_tables + static_cast<int64_t>(u.s) * p.max_blocks;
       const int blocks = (u.L + 15) >> 4;
       // block-table entries, four tiles at a time: this group's and the next's
@@ -412,13 +506,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
       for (uint32_t w = pos > C::kSlots ? pos - C::kSlots : 0; w < pos; ++w)
         mbar_wait(&kv_full[w % C::kSlots], (w / C::kSlots) & 1, nullptr, p.err);
   } else if (warp == 3) {
-    // ============== q producer, and the item that crosses out ==============
+    // =========================== q producer ===========================
     uint32_t qi = 0;
-    long long at = begin;
-    int4 border = make_int4(-1, 0, 0, 0);
-    while (walk.get(p, u)) {
+    while (next_unit(true)) {
       const int tiles = u.pair ? 2 : 1;
-      for (int h = 0; h < tiles; ++h, ++qi) {
+      for (int h = 0; h < tiles; ++h) {
         const int qs = qi % kQSlots;
         mbar_wait(&q_empty[qs], ((qi / kQSlots) & 1) ^ 1, abort_flag, p.err);
         if (*abort_flag) break;
@@ -430,12 +522,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
           if (D == 128) tma_load_3d(dst + kRegion, &p.tm_q, 64, u.g * p.group, token, &q_full[qs]);
         }
         __syncwarp();
+        ++qi;
       }
-      if (u.tile0 == 0 && u.nt < u.tiles)
-        border = make_int4(u.s, u.g, u.rp, static_cast<int>((at + u.tiles - 1) / chunk));
-      at += u.nt;
     }
-    if (lane == 0) p.border[blockIdx.x] = border;
     if (*abort_flag && lane == 0)
       for (uint32_t w = qi > kQSlots ? qi - kQSlots : 0; w < qi; ++w)
         mbar_wait(&q_full[w % kQSlots], (w / kQSlots) & 1, nullptr, p.err);
@@ -453,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
       // slot << 2 | slot << 3 | slot phase << 6 | unit parity << 7
       uint32_t fifo = 0;
       int pending = 0;
-      uint32_t n_s[2] = {0, 0}, n_pv[2] = {0, 0};  // steps of each stream issued
+      uint32_t n_s = 0, n_pv = 0;  // parity of each stream's steps issued, bit h
       uint32_t qi = 0, unit = 0;
       int w = 0, steps = 0;
       int k_slot = 0;
@@ -467,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
           const bool first = (fifo >> 1) & 1;
           const int slot = (fifo >> 3) & 7;
           if (mbar_test_wait(&kv_full[slot], (fifo >> 6) & 1) &&
-              mbar_test_wait(&p_full[h], (h ? n_pv[1] : n_pv[0]) & 1) &&
+              mbar_test_wait(&p_full[h], (n_pv >> h) & 1) &&
               (!first || mbar_test_wait(o_free, ((fifo >> 7) & 1) ^ 1))) {
             tc_fence_after();
             const uint64_t vb = desc_add(dv0, slot * C::kTileBytes);
@@ -483,17 +572,17 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
                       kIdescO, 1u);
             umma_commit(&pv_done[h]);
             if ((fifo >> 2) & 1) umma_commit(&kv_empty[slot]);
-            if (h)
-              ++n_pv[1];
-            else
-              ++n_pv[0];
+            n_pv ^= 1u << h;
             fifo >>= 8;
             --pending;
             prog = true;
           }
         }
-        if (!have && !s_end) {
-          have = walk.get(p, u);
+        // (the unit is waited for in place: nothing is issued meanwhile, so only
+        // when there is no P.V to issue either, or the unit is there)
+        if (!have && !s_end &&
+            (pending == 0 || mbar_test_wait(&u_full[u_at % kUnits], (u_at / kUnits) & 1))) {
+          have = next_unit(false);
           s_end = !have;
           w = 0;
           steps = u.pair ? 2 * u.nt : u.nt;
@@ -503,10 +592,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
           const int h = w & 1;
           const uint32_t qq = u.pair ? qi + h : qi;
           const int qs = qq % kQSlots;
-          const uint32_t mine = h ? n_s[1] : n_s[0];
           // scores replace the weights of the stream's last step: its P.V is done
           if (pending < 2 && mbar_test_wait(&kv_full[k_slot], k_phase) &&
-              mbar_test_wait(&pv_done[h], (mine & 1) ^ 1) &&
+              mbar_test_wait(&pv_done[h], ((n_s >> h) & 1) ^ 1) &&
               mbar_test_wait(&q_full[qs], (qq / kQSlots) & 1)) {
             tc_fence_after();
             const uint64_t qa = desc_add(dq0, qs * C::kTileBytes);
@@ -531,10 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
                                   (v_phase << 6) | ((unit & 1) << 7);
             fifo |= info << (8 * pending);
             ++pending;
-            if (h)
-              ++n_s[1];
-            else
-              ++n_s[0];
+            n_s ^= 1u << h;
             if (tile_end) {
               umma_commit(&kv_empty[k_slot]);
               k_slot = v_slot + 1;
@@ -565,30 +650,42 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
       }
       umma_commit(drain);
       mbar_wait(drain, 0, nullptr, p.err);
+      if (!s_end)  // aborted: the ring runs to its end
+        while (next_unit(false)) {
+        }
     }
     __syncwarp();
-  } else if (warp >= 4) {
+  } else {
     // ============================ softmax ============================
-    const int h = (warp - 4) >> 2;
+    const int wg = (warp - 4) >> 2;
+    const int h = wg >> 1;     // stream
+    const int half = wg & 1;   // keys 64 half .. of every tile
     const int q4 = warp & 3;
     const int r = q4 * 32 + lane;  // row of the tile, TMEM lane
     const uint32_t lane_addr = static_cast<uint32_t>(q4 * 32) << 16;
-    const uint32_t scol = tmem + lane_addr + h * 128;
-    const uint32_t o_col[2] = {tmem + lane_addr + kOCol, tmem + lane_addr + kOCol + 128};
+    const uint32_t scol = tmem + lane_addr + h * 128 + 64 * half;
+    const uint32_t ocol = tmem + lane_addr + kOCol + h * 128;
     const int ti = r / p.group;  // token of this row within its tile
-    const int head = r - ti * p.group;
-    const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
+    const float sc = p.scale_log2;
+    const float2 sc2 = make_float2(sc, sc);
     const float2 neg1 = make_float2(-1.f, -1.f);
-    uint32_t cnt = 0;         // this stream's steps
-    uint32_t kt0 = 0;         // ring number of the unit's first tile
+    float* x_own = xbuf + (2 * h + half) * 128 + r;
+    float* x_other = xbuf + (2 * h + (half ^ 1)) * 128 + r;
+    uint32_t cnt = 0;  // this stream's steps
+    uint32_t kt0 = 0;  // ring number of the unit's first tile
     // Tail tiles so far: two records of them are in use in turn, so one is only
     // written again when everybody has passed the other's barrier.
     uint32_t split_tails = 0, pair_tails = 0;
-    while (walk.get(p, u)) {
+    while (next_unit(true)) {
       const int i0 = u.i0 + (u.pair ? h * p.tpt : 0);
       const bool row_ok = r < rows_box && i0 + ti < u.n;
       const bool warp_ok = __any_sync(0xffffffffu, row_ok);
       const uint32_t* mrow = p.mask + static_cast<int64_t>(u.q0 + i0 + ti) * p.mask_words;
+      uint2 mhead = make_uint2(0, 0);
+      if (row_ok) {
+        mhead.x = __ldg(mrow);
+        if (u.n > 32) mhead.y = __ldg(mrow + 1);
+      }
       const int steps = u.pair ? u.nt : (u.nt - h + 1) >> 1;
       float m = -CUDART_INF_F, l = 0.f;
       bool bad = false;  // this row sees a drafted token whose V is not finite
@@ -604,118 +701,130 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
         // pages were all loaded is whole: every row sees every key.
         const bool tail = kv0 + 128 > u.c;
         const bool whole = !tail && vm == 0xffu;
-        uint32_t vis[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+        uint32_t vis[2] = {0xffffffffu, 0xffffffffu};
         if (!whole) {
           volatile uint32_t* pw =
-              poison_s + ((u.pair ? 4 : 2 * h) + ((u.pair ? pair_tails : split_tails) & 1)) * 4;
+              poison_s + ((u.pair ? 4 : 2 * h) + ((u.pair ? pair_tails : split_tails) & 1)) * 8;
           if (!u.pair || h == 0) {
-            // Thread r looks after key row r of V: zero past the context and in
-            // pages that were not loaded (their weights are 0, and 0 times what
-            // is there could be NaN), and zero, on record, where a drafted
-            // token's V is not finite (rows that do not see it have weight 0).
+            // Thread (half, r) looks after that 64-dim half of key row r of V:
+            // zero past the context and in pages that were not loaded (their
+            // weights are 0, and 0 times what is there could be NaN), and zero,
+            // on record, where a drafted token's V is not finite (rows that do
+            // not see it have weight 0).
             const int key = kv0 + r;
             const uint32_t vpos = 2 * kt + 1;
             const int vs = vpos % C::kSlots;
             mbar_wait(&kv_full[vs], (vpos / C::kSlots) & 1, abort_flag, p.err);
             const bool dead = key >= u.L || !((vm >> (r >> 4)) & 1u);
             const uint32_t vrow = sbase + C::kOffKV + vs * C::kTileBytes + (r >> 4) * C::kPage +
-                                  (r & 15) * 128;
+                                  half * 2048 + (r & 15) * 128;
             bool odd = false;
-            if (!dead && key >= u.c) {
-#pragma unroll 1
-              for (int half = 0; half < C::kHalves; ++half)
-#pragma unroll
+            if (half < C::kHalves) {
+              if (!dead && key >= u.c) {
+#pragma unroll 4
                 for (int j = 0; j < 8; ++j) {
-                  const uint4 x = lds128(vrow + half * 2048 + j * 16);
+                  const uint4 x = lds128(vrow + j * 16);
                   odd |= nonfinite_pair(x.x) | nonfinite_pair(x.y) | nonfinite_pair(x.z) |
                          nonfinite_pair(x.w);
                 }
-            }
-            if (dead || odd) {
-#pragma unroll 1
-              for (int half = 0; half < C::kHalves; ++half)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) sts128_zero(vrow + half * 2048 + j * 16);
-              fence_proxy_async_smem();
+              }
+              if (dead || odd) {
+#pragma unroll 4
+                for (int j = 0; j < 8; ++j) sts128_zero(vrow + j * 16);
+                fence_proxy_async_smem();
+              }
             }
             const uint32_t word = __ballot_sync(0xffffffffu, odd);
-            if (tail && lane == 0) pw[q4] = word;
+            if (tail && lane == 0) pw[half * 4 + q4] = word;
           }
           if (tail) {
-            named_bar_sync(u.pair ? kBarTail + 2 : kBarTail + h, u.pair ? 256 : 128);
+            named_bar_sync(u.pair ? kBarBoth : kBarStream + h, u.pair ? 512 : 256);
             if (u.pair)
               ++pair_tails;
             else
               ++split_tails;
           }
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t pages = (((vm >> (2 * j)) & 1u) ? 0x0000ffffu : 0u) |
-                                   (((vm >> (2 * j + 1)) & 1u) ? 0xffff0000u : 0u);
-            vis[j] = row_ok ? visible32(mrow, kv0 + 32 * j - u.c, u.n) & pages : 0u;
-            if (tail) bad |= (vis[j] & pw[j]) != 0;
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t two = vm >> (4 * half + 2 * j);
+            const uint32_t pages = ((two & 1u) ? 0x0000ffffu : 0u) | ((two & 2u) ? 0xffff0000u : 0u);
+            vis[j] = row_ok ? visible32(mrow, mhead, kv0 + 64 * half + 32 * j - u.c, u.n) & pages : 0u;
+            if (tail) bad |= (vis[j] & (pw[2 * half + j] | pw[4 + 2 * half + j])) != 0;
+          }
+        }
+        // The maximum of this thread's 64 scores (scaled); keys that are not seen
+        // count as -inf.
+        float top = -CUDART_INF_F;
+        if (warp_ok) {
+          float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float x[32];
+            tmem_ld32(scol + 32 * j, x);
+            if (whole && sc > 0.f) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], x[i]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                mx[i & 3] = fmaxf(mx[i & 3], ((vis[j] >> i) & 1u) ? x[i] * sc : -CUDART_INF_F);
+            }
+          }
+          top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          if (whole && sc > 0.f) top *= sc;
+        }
+        // The maximum in use is raised (and O_h and l rescaled) only when a tile's
+        // exceeds it by 2^16: weights up to that cannot overflow fp32 sums, and
+        // the division by l makes the result exact either way.
+        const bool want = m == -CUDART_INF_F ? top != -CUDART_INF_F : top > m + kRaiseLog2;
+        if (barrier_any(kBarStream + h, 256, want && row_ok)) {
+          *x_own = top;
+          named_bar_sync(kBarStream + h, 256);
+          const float t = fmaxf(top, *x_other);
+          const bool raise = m == -CUDART_INF_F ? t != -CUDART_INF_F : t > m + kRaiseLog2;
+          const float f = !raise ? 1.f : m == -CUDART_INF_F ? 0.f : exp2f(m - t);
+          if (raise) m = t;
+          l *= f;
+          // the stream's last P.V is done: this step's scores came after it
+          if (k > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+#pragma unroll 1
+            for (int cc = 0; cc < D / 32; ++cc) {  // this half's D/2 columns
+              const uint32_t col = ocol + half * (D / 2) + cc * 16;
+              float ov[16];
+              tmem_ld16(col, ov);
+              uint32_t ow[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) ow[i] = __float_as_uint(ov[i] * f);
+              tmem_st16(col, ow);
+            }
           }
         }
         if (warp_ok) {
-          // The tile's maximum (scaled); keys that are not seen count as -inf.
-          float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
-#pragma unroll
-          for (int j = 0; j < 4; j += 2) {
-            float x[64];
-            tmem_ld64(scol + 32 * j, x);
-#pragma unroll
-            for (int i = 0; i < 64; i += 2) {
-              const float2 y = __fmul2_rn(make_float2(x[i], x[i + 1]), sc2);
-              x[i] = y.x;
-              x[i + 1] = y.y;
-            }
-            if (!whole) {
-#pragma unroll
-              for (int i = 0; i < 64; ++i)
-                x[i] = ((vis[j + (i >> 5)] >> (i & 31)) & 1u) ? x[i] : -CUDART_INF_F;
-            }
-#pragma unroll
-            for (int i = 0; i < 64; ++i) mx[i & 3] = fmaxf(mx[i & 3], x[i]);
-          }
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          // The maximum in use is raised (and O_h and l rescaled) only when the
-          // tile's exceeds it by 2^16: weights up to that cannot overflow fp32
-          // sums, and the division by l makes the result exact either way.
-          const bool raise = m == -CUDART_INF_F ? top != -CUDART_INF_F : top > m + kRaiseLog2;
-          if (__any_sync(0xffffffffu, raise)) {
-            const float f = !raise ? 1.f : m == -CUDART_INF_F ? 0.f : exp2f(m - top);
-            if (raise) m = top;
-            l *= f;
-            if (k > 0) {  // the stream's last P.V is done: this step's scores came after it
-#pragma unroll 1
-              for (int cc = 0; cc < D / 16; ++cc) {
-                float ov[16];
-                tmem_ld16((h ? o_col[1] : o_col[0]) + cc * 16, ov);
-                uint32_t ow[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) ow[i] = __float_as_uint(ov[i] * f);
-                tmem_st16((h ? o_col[1] : o_col[0]) + cc * 16, ow);
-              }
-            }
-          }
           // Weights, in place of the scores: per 32 keys 16 columns of P_hi and
           // 16 of P_lo.
           const float nm = m == -CUDART_INF_F ? 0.f : -m;
           const float2 nm2 = make_float2(nm, nm);
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+          for (int j = 0; j < 2; ++j) {
             float x[32];
             tmem_ld32(scol + 32 * j, x);
+            if (!whole) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                x[i] = ((vis[j] >> i) & 1u) ? fmaf(x[i], sc, nm) : -CUDART_INF_F;
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                const float2 y = __ffma2_rn(make_float2(x[i], x[i + 1]), sc2, nm2);
+                x[i] = y.x;
+                x[i + 1] = y.y;
+              }
+            }
             uint32_t w[32];
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
-              float2 y = __ffma2_rn(make_float2(x[i], x[i + 1]), sc2, nm2);
-              if (!whole) {
-                y.x = ((vis[j] >> i) & 1u) ? y.x : -CUDART_INF_F;
-                y.y = ((vis[j] >> (i + 1)) & 1u) ? y.y : -CUDART_INF_F;
-              }
-              const float2 e = make_float2(exp2f(y.x), exp2f(y.y));
+              const float2 e = make_float2(exp2f(x[i]), exp2f(x[i + 1]));
               sum[(i >> 1) & 1] = __fadd2_rn(sum[(i >> 1) & 1], e);
               const uint32_t ex = __float_as_uint(e.x), ey = __float_as_uint(e.y);
               w[i >> 1] = __byte_perm(ex, ey, 0x7632);
@@ -734,28 +843,32 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
         if (lane == 0) mbar_arrive(&p_full[h]);
       }
 
-      // End of the unit: this row's output and log-sum-exp of the unit's keys.
+      // End of the unit: this row's output and log-sum-exp of the unit's keys.  The
+      // sums of a row's two halves meet first (a sum's sign is set where the row
+      // is bad), then, in split mode, the two streams' maxima and sums.
       if (steps > 0) mbar_wait(&pv_done[h], (cnt - 1) & 1, abort_flag, p.err);
+      tc_fence_before();
+      const int bar = u.pair ? kBarStream + h : kBarBoth, bar_threads = u.pair ? 256 : 512;
+      // (behind the exchange of the last step's maxima, if there was one)
+      named_bar_sync(bar, bar_threads);
+      *x_own = bad ? -l : l;
+      named_bar_sync(bar, bar_threads);
+      const float l_other = *x_other;
+      bad |= signbit(l_other);
+      l += fabsf(l_other);
       float m0 = m, l0 = l, m1 = -CUDART_INF_F, l1 = 0.f;
       if (!u.pair) {
-        // both streams hold a part of the same rows: (m, l) are exchanged in one
-        // buffer (l with its sign set where the row is bad)
-        const float2 own = make_float2(m, bad ? -l : l);
-        float2 other;
-        tc_fence_before();
-        if (h == 1) xbuf[r] = own;
-        named_bar_sync(kBarMerge, 256);
-        if (h == 0) {
-          other = xbuf[r];
-          xbuf[r] = own;
-        }
-        named_bar_sync(kBarMerge, 256);
-        if (h == 1) other = xbuf[r];
-        bad |= signbit(other.y);
-        m0 = h == 0 ? m : other.x;
-        l0 = h == 0 ? l : fabsf(other.y);
-        m1 = h == 0 ? other.x : m;
-        l1 = h == 0 ? fabsf(other.y) : l;
+        named_bar_sync(kBarBoth, 512);
+        *x_own = half == 0 ? m : bad ? -l : l;  // [stream][0: m, 1: l]
+        named_bar_sync(kBarBoth, 512);
+        m0 = xbuf[r];
+        l0 = xbuf[128 + r];
+        m1 = xbuf[256 + r];
+        l1 = xbuf[384 + r];
+        bad = signbit(l0) | signbit(l1);
+        l0 = fabsf(l0);
+        l1 = fabsf(l1);
+        named_bar_sync(kBarBoth, 512);  // read by all before either stream writes again
       }
       tc_fence_after();
       const float M = fmaxf(m0, m1);
@@ -766,35 +879,35 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
       const bool live = !(L == 0.f);
       const float inv = bad ? CUDART_NAN_F : live ? 1.f / L : 0.f;
       const float f0 = e0 * inv, f1 = e1 * inv;
-      const float lse2 = live ? M + log2f(L) : -CUDART_INF_F;
       const bool full = u.nt == u.tiles;
-      const int64_t orow = static_cast<int64_t>(u.q0 + i0 + ti) * p.hq + u.g * p.group + head;
+      const int64_t orow =
+          static_cast<int64_t>(u.q0 + i0 + ti) * p.hq + u.g * p.group + (r - ti * p.group);
       const int64_t prow = static_cast<int64_t>(2 * blockIdx.x + (u.tile0 == 0 ? 1 : 0)) *
                                p.part_rows + (u.pair ? h * 128 : 0) + r;
-      // pair mode: all D dims of this stream's row; split mode: this warpgroup's
-      // half of the dims, from both accumulators
-      const int d0 = u.pair ? 0 : h * (D / 2);
-      const int dims = u.pair ? D : D / 2;
-      const uint32_t src = (u.pair ? (h ? o_col[1] : o_col[0]) : o_col[0]) + d0;
+      // pair mode: this half's D/2 dims of the stream's row; split mode: a quarter
+      // of the dims, from both accumulators
+      const int d0 = u.pair ? half * (D / 2) : wg * (D / 4);
+      const int dims = u.pair ? D / 2 : D / 4;
+      const uint32_t src = (u.pair ? ocol : tmem + lane_addr + kOCol) + d0;
       const bool two = !u.pair && u.nt > 1;  // stream 1 had a tile
       if (warp_ok) {
 #pragma unroll 1
-        for (int cc = 0; cc < dims; cc += 32) {
-          float a[32];
-          tmem_ld32(src + cc, a);
+        for (int cc = 0; cc < dims; cc += 16) {
+          float a[16];
+          tmem_ld16(src + cc, a);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) a[i] *= u.pair ? inv : f0;
+          for (int i = 0; i < 16; ++i) a[i] *= f0;
           if (two) {
-            float b[32];
-            tmem_ld32(src + 128 + cc, b);
+            float b[16];
+            tmem_ld16(src + 128 + cc, b);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) a[i] = fmaf(b[i], f1, a[i]);
+            for (int i = 0; i < 16; ++i) a[i] = fmaf(b[i], f1, a[i]);
           }
           // nothing seen: the accumulator of all-zero weights is zero, and stays so
           if (row_ok && full) {
             uint4* dst = reinterpret_cast<uint4*>(p.out + orow * D + d0 + cc);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 2; ++i)
               dst[i] = make_uint4(pack_bf16x2(a[8 * i], a[8 * i + 1]),
                                   pack_bf16x2(a[8 * i + 2], a[8 * i + 3]),
                                   pack_bf16x2(a[8 * i + 4], a[8 * i + 5]),
@@ -802,7 +915,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
           } else if (row_ok) {
             float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + d0 + cc);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < 4; ++i)
               dst[i] = make_float4(a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]);
           }
         }
@@ -810,7 +923,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(o_free);
-      if (row_ok && (u.pair || h == 0)) {
+      if (row_ok && half == 0 && (u.pair || h == 0)) {
+        const float lse2 = live ? M + log2f(L) : -CUDART_INF_F;
         if (!full)
           p.part_lse[prow] = lse2;
         else if (p.lse)
