@@ -20,9 +20,9 @@
 //   split mode   (one row tile): both take the same rows, stream h the key tiles
 //                h, h+2, ...; their results meet by log-sum-exp at the end.
 // The maximum that a row's weights are formed with is the same in both halves of
-// the row and stays until a tile's maximum exceeds it by 2^16 in some row of the
-// stream: one vote per step (an OR-reducing barrier); only then the halves
-// exchange maxima and the accumulator is rescaled.
+// the row and stays until a tile's maximum exceeds it by 2^16: the two warps that
+// share 32 rows vote once per step (an OR-reducing barrier of 64 threads); only
+// then they exchange maxima and rescale their rows of the accumulator.
 //
 // Work split: all items' key tiles, in order, are one line, with kItemCost more
 // places in front of every item for what it costs besides its tiles, and every
@@ -36,12 +36,14 @@
 // the tensor cores and the softmax warps beyond.
 //
 // Roles (one CTA per SM): warp 0 copies K and V pages (one ring, K and V of a
-// tile in turn), warp 1 issues the MMAs, warp 2 walks the stretch and publishes
-// its units in a ring, warp 3 copies q, warps 4-19 are the softmax warpgroups
-// (stream, key half).  Every wait on an mbarrier is bounded.  The named barriers
-// join softmax warps that go through the same units and steps whatever happens:
-// after a time-out the data waits return at once and the unit ring, which depends
-// on nothing else, still runs to its end.
+// tile in turn), warps 1 and 2 issue the MMAs of one stream each (one warp for
+// both left the tensor cores idle for a third of the time: what it does between
+// two products is short, but every instruction of it waits among those of the
+// softmax warps), warp 3 walks the stretch, publishes its units in a ring and
+// copies their q, warps 4-19 are the softmax warpgroups (stream, key half).
+// Every wait on an mbarrier is bounded.  The named barriers join softmax warps
+// that go through the same units and steps whatever happens: after a time-out
+// the data waits return at once and the unit ring still runs to its end.
 #include <math_constants.h>
 
 #include "../../include/pa_tree.h"
@@ -60,7 +62,7 @@ constexpr int kItemCost = 2;       // places in front of an item
 constexpr int kRegion = 128 * 128; // 128 rows x 128 bytes
 constexpr int kQSlots = 2;
 constexpr int kUnits = 4;          // ring of units
-constexpr int kUnitReaders = 3 + 16;  // K/V, q, MMA, softmax warps
+constexpr int kUnitReaders = 3 + 16;  // K/V, MMA and softmax warps
 constexpr int kMaskRing = 16;
 constexpr float kRaiseLog2 = 16.f; // raise the maximum in use only past 2^16
 constexpr uint32_t kTmemCols = 512;
@@ -69,6 +71,7 @@ constexpr uint32_t kOCol = 256;    // S_h at column 128 h, O_h at 256 + 128 h
 // Named barriers.
 constexpr int kBarBoth = 1;    // all softmax warps
 constexpr int kBarStream = 2;  // + h: the warps of one stream
+constexpr int kBarPair = 4;    // + 4 h + warp: the two warps of 32 rows
 
 template <int D>
 struct Cfg {
@@ -81,13 +84,12 @@ struct Cfg {
   static constexpr int kOffUnit = kOffKV + kSlots * kTileBytes;  // [kUnits] x 48 bytes
   static constexpr int kOffX = kOffUnit + kUnits * 48;  // [4][128] floats: exchanges of a row
   static constexpr int kOffBar = kOffX + 4 * 128 * 4;
-  static constexpr int kNumBars = 2 * kQSlots + 2 * kSlots + 2 * kUnits + 6 + 2;
+  static constexpr int kNumBars = 2 * kQSlots + 2 * kSlots + 2 * kUnits + 6 + 3;
   // tensor-memory slot, abort flag, plan {sequence, place in it (8 bytes)}
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kOffMask = kOffMisc + 24;
   static constexpr int kOffPoison = kOffMask + 4 * kMaskRing;  // [3 sets][2][2 halves][4 words]
   static constexpr int kSmem = kOffPoison + 3 * 2 * 2 * 16;
-  // kWarpSums of the start-up scan use the exchange buffer
   static_assert(kSmem <= 232448, "shared memory per CTA");
 };
 
@@ -182,8 +184,8 @@ struct Unit {
 };
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-  return static_cast<uint32_t>(f32_to_bf16_bits(lo)) |
-         (static_cast<uint32_t>(f32_to_bf16_bits(hi)) << 16);
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
 }
 
 // 32 keys' visibility for one row, from key c + rel on: cached ones (rel < 0) are
@@ -199,6 +201,17 @@ __device__ __forceinline__ uint32_t mask_word(const uint32_t* row, uint2 head, i
 __device__ __forceinline__ uint32_t visible32(const uint32_t* row, uint2 head, int rel, int n) {
   const int j = rel >> 5;  // floor
   return __funnelshift_r(mask_word(row, head, j, n), mask_word(row, head, j + 1, n), rel & 31);
+}
+
+// One lane of a converged warp, always the same.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
 }
 
 // A wait of the unit ring: several times as long as the waits for data.
@@ -248,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
   uint64_t* p_full = s_full + 2;        // weights written back
   uint64_t* pv_done = p_full + 2;       // P.V complete
   uint64_t* o_free = pv_done + 2;       // both accumulators of a unit read out
-  uint64_t* drain = o_free + 1;
+  uint64_t* drain = o_free + 1;         // per stream
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
   volatile int* plan_seq = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8);
@@ -271,11 +284,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
   if (tid == 0) {
     for (int i = 0; i < kQSlots; ++i) {
       mbar_init(&q_full[i], 1);
-      mbar_init(&q_empty[i], 1);
+      mbar_init(&q_empty[i], 2);  // one arrival per stream, or two of one
     }
     for (int i = 0; i < C::kSlots; ++i) {
       mbar_init(&kv_full[i], 1);
-      mbar_init(&kv_empty[i], 1);
+      mbar_init(&kv_empty[i], 2);
     }
     for (int i = 0; i < kUnits; ++i) {
       mbar_init(&u_full[i], 1);
@@ -285,9 +298,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
       mbar_init(&s_full[h], 1);
       mbar_init(&p_full[h], 8);  // one arrival per warp of the stream
       mbar_init(&pv_done[h], 1);
+      mbar_init(&drain[h], 1);
     }
     mbar_init(o_free, 16);
-    mbar_init(drain, 1);
     *abort_flag = 0;
     prefetch_tmap(&p.tm_k);
     prefetch_tmap(&p.tm_v);
@@ -345,12 +358,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
   const uint32_t tmem = *tmem_slot;
   const int rows_box = p.tpt * p.group;
 
-  // The next unit of the ring, for a whole warp (or the MMA's lane).  Its waits do
+  // The next unit of the ring, for a whole warp.  Its waits do
   // not heed the abort flag (every role takes every unit) and outlast those that
   // set it.
   uint32_t u_at = 0;
   Unit u;
-  auto next_unit = [&](bool whole_warp) -> bool {
+  auto next_unit = [&]() -> bool {
     const int slot = u_at % kUnits;
     if (!ring_wait(&u_full[slot], (u_at / kUnits) & 1, p.err)) return false;
     const int4* src = reinterpret_cast<const int4*>(&units[slot]);
@@ -367,14 +380,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
     u.c = u.L - u.n;
     u.i0 = u.rp * 2 * p.tpt;
     u.pair = u.n - u.i0 > p.tpt;
-    if (whole_warp) __syncwarp();
-    if (!whole_warp || lane == 0) mbar_arrive(&u_empty[slot]);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&u_empty[slot]);
     ++u_at;
     return u.nt > 0;
   };
 
-  if (warp == 2) {
-    // ============ the walk along the stretch, and its border ============
+  if (warp == 3) {
+    // ====== the walk along the stretch, its border, and the q producer ======
+    uint32_t qi = 0;
     const long long begin = chunk * blockIdx.x;
     long long left = total - begin < chunk ? total - begin : chunk;  // places still to take
     long long at = begin;
@@ -441,14 +455,33 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
       __syncwarp();
       ++u_at;
       if (w.nt == 0) break;
+      const int i0 = w.rp * 2 * p.tpt;
+      const int tiles = w.n - i0 > p.tpt ? 2 : 1;
+      for (int h = 0; h < tiles; ++h) {
+        const int qs = qi % kQSlots;
+        mbar_wait(&q_empty[qs], ((qi / kQSlots) & 1) ^ 1, abort_flag, p.err);
+        if (__any_sync(0xffffffffu, *abort_flag)) break;
+        if (lane == 0) {
+          const uint32_t dst = sbase + C::kOffQ + qs * C::kTileBytes;
+          const int token = w.q0 + i0 + h * p.tpt;
+          mbar_arrive_expect_tx(&q_full[qs], C::kHalves * rows_box * 128);
+          tma_load_3d(dst, &p.tm_q, 0, w.g * p.group, token, &q_full[qs]);
+          if (D == 128) tma_load_3d(dst + kRegion, &p.tm_q, 64, w.g * p.group, token, &q_full[qs]);
+        }
+        __syncwarp();
+        ++qi;
+      }
     }
     if (lane == 0) p.border[blockIdx.x] = border;
+    if (*abort_flag && lane == 0)
+      for (uint32_t w = qi > kQSlots ? qi - kQSlots : 0; w < qi; ++w)
+        mbar_wait(&q_full[w % kQSlots], (w / kQSlots) & 1, nullptr, p.err);
   } else if (warp == 0) {
     // ======================== K and V producer ========================
     uint32_t pos = 0, kt = 0;
     int slot = 0;
     uint32_t phase = 0;
-    while (next_unit(true)) {
+    while (next_unit()) {
       const int32_t* table = p.block_tables + static_cast<int64_t>(u.s) * p.max_blocks;
       const int blocks = (u.L + 15) >> 4;
       // block-table entries, four tiles at a time: this group's and the next's
@@ -505,156 +538,87 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
     if (*abort_flag && lane == 0)  // the copies in flight land before the CTA ends
       for (uint32_t w = pos > C::kSlots ? pos - C::kSlots : 0; w < pos; ++w)
         mbar_wait(&kv_full[w % C::kSlots], (w / C::kSlots) & 1, nullptr, p.err);
-  } else if (warp == 3) {
-    // =========================== q producer ===========================
-    uint32_t qi = 0;
-    while (next_unit(true)) {
-      const int tiles = u.pair ? 2 : 1;
-      for (int h = 0; h < tiles; ++h) {
-        const int qs = qi % kQSlots;
-        mbar_wait(&q_empty[qs], ((qi / kQSlots) & 1) ^ 1, abort_flag, p.err);
-        if (*abort_flag) break;
-        if (lane == 0) {
-          const uint32_t dst = sbase + C::kOffQ + qs * C::kTileBytes;
-          const int token = u.q0 + u.i0 + h * p.tpt;
-          mbar_arrive_expect_tx(&q_full[qs], C::kHalves * rows_box * 128);
-          tma_load_3d(dst, &p.tm_q, 0, u.g * p.group, token, &q_full[qs]);
-          if (D == 128) tma_load_3d(dst + kRegion, &p.tm_q, 64, u.g * p.group, token, &q_full[qs]);
+  } else if (warp < 3) {
+    // ============================= MMA ==============================
+    // Warp 1 + h issues stream h's products: the scores of a step, then, when its
+    // weights are written, P.V, then the next step's scores once that has read
+    // them.  The whole warp goes along with the same values and one lane issues,
+    // so the descriptors stay in uniform registers.
+    const int h = warp - 1;
+    const uint32_t ubase = __shfl_sync(0xffffffffu, sbase, 0);
+    const uint32_t utmem = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint64_t dq0 = smem_desc_sw128(ubase + C::kOffQ, 16, 1024);
+    const uint64_t dk0 = smem_desc_sw128(ubase + C::kOffKV, 16, 1024);
+    const uint64_t dv0 = smem_desc_sw128(ubase + C::kOffKV, 2048, 1024);
+    const uint32_t s_col = utmem + h * 128, o_col = utmem + kOCol + h * 128;
+    uint32_t cnt = 0;   // this stream's steps
+    uint32_t qi = 0, unit = 0, kt0 = 0;
+    while (next_unit()) {
+      const bool pair = __shfl_sync(0xffffffffu, u.pair ? 1 : 0, 0);
+      const int nt = __shfl_sync(0xffffffffu, u.nt, 0);
+      const int steps = pair ? nt : (nt - h + 1) >> 1;
+      // in pair mode both streams read a K or V slot, and one a q slot; in split
+      // mode the other way round: either way two arrivals free it
+      const bool kv_twice = !pair, q_twice = pair || nt == 1;
+      const uint32_t qq = pair ? qi + h : qi;
+      const int qs = qq % kQSlots;
+      const uint64_t qa = desc_add(dq0, qs * C::kTileBytes);
+      if (steps > 0)
+        mbar_wait(&q_full[qs], (qq / kQSlots) & 1, abort_flag, p.err);
+      else  // (every unit's, so its parity is never taken for another's)
+        mbar_wait(o_free, (unit & 1) ^ 1, abort_flag, p.err);
+      for (int k = 0; k < steps; ++k, ++cnt) {
+        const uint32_t kpos = 2 * (kt0 + (pair ? k : 2 * k + h));
+        const int ks = kpos % C::kSlots, vs = (kpos + 1) % C::kSlots;
+        mbar_wait(&kv_full[ks], (kpos / C::kSlots) & 1, abort_flag, p.err);
+        // scores replace the weights of the stream's last step: its P.V is done
+        mbar_wait(&pv_done[h], (cnt & 1) ^ 1, abort_flag, p.err);
+        if (__any_sync(0xffffffffu, *abort_flag)) continue;
+        tc_fence_after();
+        const uint64_t kb = desc_add(dk0, ks * C::kTileBytes);
+        if (elect_one()) {
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            const uint32_t off = (i >> 2) * kRegion + (i & 3) * 32;
+            umma_ss(s_col, desc_add(qa, off), desc_add(kb, off), kIdescS, i > 0 ? 1u : 0u);
+          }
+          umma_commit(&s_full[h]);
+          umma_commit(&kv_empty[ks]);
+          if (kv_twice) umma_commit(&kv_empty[ks]);
+          if (k == steps - 1) {
+            umma_commit(&q_empty[qs]);
+            if (q_twice) umma_commit(&q_empty[qs]);
+          }
         }
         __syncwarp();
-        ++qi;
+        mbar_wait(&kv_full[vs], ((kpos + 1) / C::kSlots) & 1, abort_flag, p.err);
+        if (k == 0) mbar_wait(o_free, (unit & 1) ^ 1, abort_flag, p.err);
+        mbar_wait(&p_full[h], cnt & 1, abort_flag, p.err);
+        if (__any_sync(0xffffffffu, *abort_flag)) continue;
+        tc_fence_after();
+        const uint64_t vb = desc_add(dv0, vs * C::kTileBytes);
+        if (elect_one()) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            umma_ts(o_col, s_col + 32 * (i >> 1) + 8 * (i & 1), desc_add(vb, i * C::kPage),
+                    kIdescO, k == 0 && i == 0 ? 0u : 1u);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            umma_ts(o_col, s_col + 32 * (i >> 1) + 8 * (i & 1) + 16, desc_add(vb, i * C::kPage),
+                    kIdescO, 1u);
+          umma_commit(&pv_done[h]);
+          umma_commit(&kv_empty[vs]);
+          if (kv_twice) umma_commit(&kv_empty[vs]);
+        }
+        __syncwarp();
       }
+      qi += pair ? 2 : 1;
+      ++unit;
+      kt0 += nt;
     }
-    if (*abort_flag && lane == 0)
-      for (uint32_t w = qi > kQSlots ? qi - kQSlots : 0; w < qi; ++w)
-        mbar_wait(&q_full[w % kQSlots], (w / kQSlots) & 1, nullptr, p.err);
-  } else if (warp == 1) {
-    // ============================= MMA ==============================
-    // One lane issues the scores of the next step and the P.V of an earlier one,
-    // each as soon as its inputs are there (non-blocking polls, one limit on time
-    // without progress).  Steps are taken in the order (key tile, stream).
-    if (lane == 0) {
-      const uint64_t dq0 = smem_desc_sw128(sbase + C::kOffQ, 16, 1024);
-      const uint64_t dk0 = smem_desc_sw128(sbase + C::kOffKV, 16, 1024);
-      const uint64_t dv0 = smem_desc_sw128(sbase + C::kOffKV, 2048, 1024);
-      // steps whose scores are issued and whose P.V is not (two at most), oldest
-      // in the low byte: stream | first of its unit << 1 | last reader of its V
-      // slot << 2 | slot << 3 | slot phase << 6 | unit parity << 7
-      uint32_t fifo = 0;
-      int pending = 0;
-      uint32_t n_s = 0, n_pv = 0;  // parity of each stream's steps issued, bit h
-      uint32_t qi = 0, unit = 0;
-      int w = 0, steps = 0;
-      int k_slot = 0;
-      uint32_t k_phase = 0;  // K of the current tile in the ring
-      bool have = false, s_end = false;
-      long long last = clock64();
-      while (!*abort_flag) {
-        bool prog = false;
-        if (pending > 0) {
-          const int h = fifo & 1;
-          const bool first = (fifo >> 1) & 1;
-          const int slot = (fifo >> 3) & 7;
-          if (mbar_test_wait(&kv_full[slot], (fifo >> 6) & 1) &&
-              mbar_test_wait(&p_full[h], (n_pv >> h) & 1) &&
-              (!first || mbar_test_wait(o_free, ((fifo >> 7) & 1) ^ 1))) {
-            tc_fence_after();
-            const uint64_t vb = desc_add(dv0, slot * C::kTileBytes);
-            const uint32_t sp = tmem + h * 128;
-            const uint32_t oc = tmem + kOCol + h * 128;
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              umma_ts(oc, sp + 32 * (k >> 1) + 8 * (k & 1), desc_add(vb, k * C::kPage), kIdescO,
-                      first && k == 0 ? 0u : 1u);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              umma_ts(oc, sp + 32 * (k >> 1) + 8 * (k & 1) + 16, desc_add(vb, k * C::kPage),
-                      kIdescO, 1u);
-            umma_commit(&pv_done[h]);
-            if ((fifo >> 2) & 1) umma_commit(&kv_empty[slot]);
-            n_pv ^= 1u << h;
-            fifo >>= 8;
-            --pending;
-            prog = true;
-          }
-        }
-        // (the unit is waited for in place: nothing is issued meanwhile, so only
-        // when there is no P.V to issue either, or the unit is there)
-        if (!have && !s_end &&
-            (pending == 0 || mbar_test_wait(&u_full[u_at % kUnits], (u_at / kUnits) & 1))) {
-          have = next_unit(false);
-          s_end = !have;
-          w = 0;
-          steps = u.pair ? 2 * u.nt : u.nt;
-          prog = true;
-        }
-        if (have) {
-          const int h = w & 1;
-          const uint32_t qq = u.pair ? qi + h : qi;
-          const int qs = qq % kQSlots;
-          // scores replace the weights of the stream's last step: its P.V is done
-          if (pending < 2 && mbar_test_wait(&kv_full[k_slot], k_phase) &&
-              mbar_test_wait(&pv_done[h], ((n_s >> h) & 1) ^ 1) &&
-              mbar_test_wait(&q_full[qs], (qq / kQSlots) & 1)) {
-            tc_fence_after();
-            const uint64_t qa = desc_add(dq0, qs * C::kTileBytes);
-            const uint64_t kb = desc_add(dk0, k_slot * C::kTileBytes);
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const uint32_t off = (k >> 2) * kRegion + (k & 3) * 32;
-              umma_ss(tmem + h * 128, desc_add(qa, off), desc_add(kb, off), kIdescS,
-                      k > 0 ? 1u : 0u);
-            }
-            umma_commit(&s_full[h]);
-            int v_slot = k_slot + 1;
-            uint32_t v_phase = k_phase;
-            if (v_slot == C::kSlots) {
-              v_slot = 0;
-              v_phase ^= 1;
-            }
-            const bool tile_end = !u.pair || h == 1;
-            const bool first = w < 2;
-            const uint32_t info = static_cast<uint32_t>(h) | (first ? 2u : 0u) |
-                                  (tile_end ? 4u : 0u) | (static_cast<uint32_t>(v_slot) << 3) |
-                                  (v_phase << 6) | ((unit & 1) << 7);
-            fifo |= info << (8 * pending);
-            ++pending;
-            n_s ^= 1u << h;
-            if (tile_end) {
-              umma_commit(&kv_empty[k_slot]);
-              k_slot = v_slot + 1;
-              k_phase = v_phase;
-              if (k_slot == C::kSlots) {
-                k_slot = 0;
-                k_phase ^= 1;
-              }
-            }
-            ++w;
-            // the unit's last use of this q tile
-            if (u.pair ? w >= steps - 1 : w == steps) umma_commit(&q_empty[qs]);
-            if (w == steps) {
-              qi += u.pair ? 2 : 1;
-              ++unit;
-              have = false;
-            }
-            prog = true;
-          }
-        }
-        if (s_end && pending == 0) break;
-        if (prog) {
-          last = clock64();
-        } else if (clock64() - last > kWaitLimitCycles) {
-          *abort_flag = 1;
-          raise_error(p.err, PA_DEV_ERR_TIMEOUT);
-        }
-      }
-      umma_commit(drain);
-      mbar_wait(drain, 0, nullptr, p.err);
-      if (!s_end)  // aborted: the ring runs to its end
-        while (next_unit(false)) {
-        }
-    }
+    if (elect_one()) umma_commit(&drain[h]);
     __syncwarp();
+    mbar_wait(&drain[h], 0, nullptr, p.err);
   } else {
     // ============================ softmax ============================
     const int wg = (warp - 4) >> 2;
@@ -666,7 +630,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
     const uint32_t scol = tmem + lane_addr + h * 128 + 64 * half;
     const uint32_t ocol = tmem + lane_addr + kOCol + h * 128;
     const int ti = r / p.group;  // token of this row within its tile
-    const float sc = p.scale_log2;
+    // a scale of 0 becomes the smallest there is, which keeps infinities
+    const float sc = p.scale_log2 == 0.f ? 1.2e-38f : p.scale_log2;
+    const float unseen = sc > 0.f ? -CUDART_INF_F : CUDART_INF_F;
     const float2 sc2 = make_float2(sc, sc);
     const float2 neg1 = make_float2(-1.f, -1.f);
     float* x_own = xbuf + (2 * h + half) * 128 + r;
@@ -676,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
     // Tail tiles so far: two records of them are in use in turn, so one is only
     // written again when everybody has passed the other's barrier.
     uint32_t split_tails = 0, pair_tails = 0;
-    while (next_unit(true)) {
+    while (next_unit()) {
       const int i0 = u.i0 + (u.pair ? h * p.tpt : 0);
       const bool row_ok = r < rows_box && i0 + ti < u.n;
       const bool warp_ok = __any_sync(0xffffffffu, row_ok);
@@ -752,34 +718,46 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
             if (tail) bad |= (vis[j] & (pw[2 * half + j] | pw[4 + 2 * half + j])) != 0;
           }
         }
-        // The maximum of this thread's 64 scores (scaled); keys that are not seen
-        // count as -inf.
-        float top = -CUDART_INF_F;
-        if (warp_ok) {
-          float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
-#pragma unroll
+        // Scores of keys that are not seen become infinite in place, of the sign
+        // that scales to -inf: from here on every tile is alike.  (Loops of 32
+        // columns, not unrolled: the hot code of 20 warps in different roles has
+        // to fit the instruction caches.)
+        if (!whole && warp_ok) {
+#pragma unroll 1
           for (int j = 0; j < 2; ++j) {
             float x[32];
             tmem_ld32(scol + 32 * j, x);
-            if (whole && sc > 0.f) {
+            uint32_t w[32];
+            const uint32_t v = j ? vis[1] : vis[0];
 #pragma unroll
-              for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], x[i]);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                mx[i & 3] = fmaxf(mx[i & 3], ((vis[j] >> i) & 1u) ? x[i] * sc : -CUDART_INF_F);
-            }
+            for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(((v >> i) & 1u) ? x[i] : unseen);
+            tmem_st32_nowait(scol + 32 * j, w);
           }
-          top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          if (whole && sc > 0.f) top *= sc;
+          tmem_wait_st();
+        }
+        // The maximum of this thread's 64 scores (scaled).
+        float top = -CUDART_INF_F;
+        if (warp_ok) {
+#pragma unroll 1
+          for (int j = 0; j < 2; ++j) {
+            float x[32];
+            tmem_ld32(scol + 32 * j, x);
+            float mx[2] = {-CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float2 y = __fmul2_rn(make_float2(x[i], x[i + 1]), sc2);
+              mx[(i >> 1) & 1] = fmaxf(mx[(i >> 1) & 1], fmaxf(y.x, y.y));
+            }
+            top = fmaxf(top, fmaxf(mx[0], mx[1]));
+          }
         }
         // The maximum in use is raised (and O_h and l rescaled) only when a tile's
         // exceeds it by 2^16: weights up to that cannot overflow fp32 sums, and
         // the division by l makes the result exact either way.
         const bool want = m == -CUDART_INF_F ? top != -CUDART_INF_F : top > m + kRaiseLog2;
-        if (barrier_any(kBarStream + h, 256, want && row_ok)) {
+        if (barrier_any(kBarPair + 4 * h + q4, 64, want && row_ok)) {
           *x_own = top;
-          named_bar_sync(kBarStream + h, 256);
+          named_bar_sync(kBarPair + 4 * h + q4, 64);
           const float t = fmaxf(top, *x_other);
           const bool raise = m == -CUDART_INF_F ? t != -CUDART_INF_F : t > m + kRaiseLog2;
           const float f = !raise ? 1.f : m == -CUDART_INF_F ? 0.f : exp2f(m - t);
@@ -805,26 +783,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
           const float nm = m == -CUDART_INF_F ? 0.f : -m;
           const float2 nm2 = make_float2(nm, nm);
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
+#pragma unroll 1
           for (int j = 0; j < 2; ++j) {
             float x[32];
             tmem_ld32(scol + 32 * j, x);
-            if (!whole) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                x[i] = ((vis[j] >> i) & 1u) ? fmaf(x[i], sc, nm) : -CUDART_INF_F;
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                const float2 y = __ffma2_rn(make_float2(x[i], x[i + 1]), sc2, nm2);
-                x[i] = y.x;
-                x[i + 1] = y.y;
-              }
-            }
             uint32_t w[32];
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
-              const float2 e = make_float2(exp2f(x[i]), exp2f(x[i + 1]));
+              const float2 y = __ffma2_rn(make_float2(x[i], x[i + 1]), sc2, nm2);
+              const float2 e = make_float2(exp2f(y.x), exp2f(y.y));
               sum[(i >> 1) & 1] = __fadd2_rn(sum[(i >> 1) & 1], e);
               const uint32_t ex = __float_as_uint(e.x), ey = __float_as_uint(e.y);
               w[i >> 1] = __byte_perm(ex, ey, 0x7632);
