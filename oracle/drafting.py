@@ -102,13 +102,13 @@ def attention_mass(q, lse, cu, k_pool, tables, lens, scale: float):
 def evict_choice(mass, length: int, budget: int, sink: int, recent: int):
     """Indices kept, ascending: ``min(length, budget)`` tokens -- the first
     ``sink``, the last ``recent``, then the heaviest others (the lowest index
-    first among equals; NaN counts as the least)."""
+    first among equals; NaN counts as less than -inf)."""
     keep = min(int(length), max(int(budget), 0))
     sink = min(keep, sink)
     recent = min(keep - sink, recent)
     forced = list(range(sink)) + list(range(length - recent, length))
-    value = lambda t: -np.inf if np.isnan(mass[t]) else float(mass[t])  # noqa: E731
-    others = sorted(range(sink, length - recent), key=lambda t: (-value(t), t))
+    value = lambda t: (1, 0.0) if np.isnan(mass[t]) else (0, -float(mass[t]))  # noqa: E731
+    others = sorted(range(sink, length - recent), key=lambda t: (value(t), t))
     return np.array(sorted(forced + others[:keep - len(forced)]), np.int64)
 
 

@@ -24,6 +24,7 @@ __all__ = [
     "pa_read_probe",
     "pa_rope", "pa_rope_and_cache", "pa_rope_frequencies",
     "pa_tree_attention", "pa_tree_workspace_size",
+    "pa_attention_mass", "pa_evict", "pa_compact_tokens",
     "pool_desc", "lib",
     "PaError", "PA_KERNEL_AUTO", "PA_KERNEL_SIMT", "PA_KERNEL_TCGEN05",
     "PA_PREFILL_EXACT_WEIGHTS",
@@ -308,7 +309,7 @@ def pa_read_probe(k_pool, v_pool, block_tables, context_lens, num_ctas=None, out
 
 
 # ----------------------------------------------------------------------------
-# Drafting and eviction (include/pa_rope.h, include/pa_tree.h)
+# Drafting and eviction (include/pa_rope.h, include/pa_tree.h, include/pa_evict.h)
 #
 # These calls run on the device their tensors are on (whatever the current one)
 # and, without a `stream`, on that device's current stream; what they allocate
@@ -526,3 +527,129 @@ def pa_tree_attention(q, cu_q_lens, max_q_len, tree_mask, k_pool, v_pool, block_
          v_pool.data_ptr(), desc, block_tables.data_ptr(), blocks, context_lens.data_ptr(), seqs,
          hq, float(scale), out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel())
     return out, lse
+
+
+def pa_attention_mass(q, lse, cu_q_lens, max_q_len, k_pool, block_tables, context_lens, scale,
+                      mass_in=None, mass=None, stream=None):
+    """Add to every cached token the softmax weights that the rows of ``q`` (bf16
+    [total_q, Hq, D], with the ``lse`` fp32 [total_q, Hq] their attention returned)
+    gave it.  ``cu_q_lens`` int32 [S+1] on the device, or None for a decode step
+    (one row per sequence).  ``mass_in``: fp32 [S, Hkv, W] so far (None: zeros);
+    ``mass``: where the sums go (may be ``mass_in``; default: a new tensor, zero
+    past each sequence's length).  Returns ``mass``."""
+    torch = _torch()
+    dev = q.device
+    f32 = torch.float32
+    qs = _rows_arg("q", q, dev)
+    total_q, hq, d = q.shape
+    desc, seqs, blocks = _batch_args(k_pool, block_tables, context_lens, dev)
+    if desc.head_dim != d:
+        raise ValueError(f"q has head_dim {d}, the pool {desc.head_dim}")
+    _arg("lse", lse, f32, dev, (total_q, hq))
+    if cu_q_lens is not None:
+        _arg("cu_q_lens", cu_q_lens, torch.int32, dev, (seqs + 1,))
+    if mass_in is not None:
+        _arg("mass_in", mass_in, f32, dev)
+        _dims("mass_in", mass_in, 3)
+    if mass is None:
+        shape = (seqs, desc.num_kv_heads,
+                 blocks * desc.block_size if mass_in is None else mass_in.shape[2])
+        mass = _empty(shape, f32, dev, stream)
+        with torch.cuda.stream(stream):  # (None: the current one)
+            mass.zero_()
+    else:
+        _arg("mass", mass, f32, dev)
+        _dims("mass", mass, 3)
+    width = mass.shape[2]
+    if mass.shape != (seqs, desc.num_kv_heads, width) or (
+            mass_in is not None and mass_in.shape != mass.shape):
+        raise ValueError(f"mass and mass_in must be [{seqs}, {desc.num_kv_heads}, W] alike")
+    _run("pa_attention_mass", dev, stream, q.data_ptr(), qs, lse.data_ptr(), _ptr(cu_q_lens),
+         total_q, int(max_q_len), k_pool.data_ptr(), desc, block_tables.data_ptr(), blocks,
+         context_lens.data_ptr(), seqs, hq, float(scale), _ptr(mass_in), mass.data_ptr(), width)
+    return mass
+
+
+def pa_evict(mass, k_pool, v_pool, block_tables, context_lens, budgets, sink=0, recent=0,
+             new_tables=None, kept=None, new_lens=None, mass_out=None, max_keep=None, stream=None):
+    """Bring every sequence down to ``budgets`` (int32 [S]) tokens per KV head: the
+    first ``sink``, the last ``recent`` and the heaviest others by ``mass`` (fp32
+    [S, Hkv, W]), packed in order in place or into the blocks of ``new_tables``
+    (int32 [S, blocks]).  Returns ``(kept, new_lens, mass_out)``: the kept tokens'
+    indices (int32 [S, Hkv, K]), the new lengths (int32 [S]) and the kept tokens'
+    weights (fp32 [S, Hkv, K]); what is past a new length in them is not written.
+    K comes from ``kept``, or else is ``max_keep`` (default: W), an upper bound of
+    the budgets."""
+    torch = _torch()
+    dev = mass.device
+    desc, seqs, blocks = _batch_args(k_pool, block_tables, context_lens, dev)
+    _arg("v_pool", v_pool, torch.bfloat16, dev, k_pool.shape)
+    _arg("mass", mass, torch.float32, dev)
+    _dims("mass", mass, 3)
+    hkv = desc.num_kv_heads
+    width = mass.shape[2]
+    if mass.shape != (seqs, hkv, width):
+        raise ValueError(f"mass must be [{seqs}, {hkv}, W], got {list(mass.shape)}")
+    _arg("budgets", budgets, torch.int32, dev, (seqs,))
+    new_blocks = 0
+    if new_tables is not None:
+        _arg("new_tables", new_tables, torch.int32, dev)
+        _dims("new_tables", new_tables, 2)
+        if new_tables.shape[0] != seqs:
+            raise ValueError(f"new_tables must have {seqs} rows, got {new_tables.shape[0]}")
+        new_blocks = new_tables.shape[1]
+    if kept is None:
+        keep = width if max_keep is None else int(max_keep)
+        kept = _empty((seqs, hkv, keep), torch.int32, dev, stream)
+    else:
+        _arg("kept", kept, torch.int32, dev)
+        _dims("kept", kept, 3)
+        keep = kept.shape[2]
+        if kept.shape != (seqs, hkv, keep):
+            raise ValueError(f"kept must be [{seqs}, {hkv}, K], got {list(kept.shape)}")
+    if new_lens is None:
+        new_lens = _empty((seqs,), torch.int32, dev, stream)
+    else:
+        _arg("new_lens", new_lens, torch.int32, dev, (seqs,))
+    if mass_out is None:
+        mass_out = _empty((seqs, hkv, keep), torch.float32, dev, stream)
+    else:
+        _arg("mass_out", mass_out, torch.float32, dev)
+        _dims("mass_out", mass_out, 3)
+        if mass_out.shape[:2] != (seqs, hkv):
+            raise ValueError(f"mass_out must be [{seqs}, {hkv}, K], got {list(mass_out.shape)}")
+    _run("pa_evict", dev, stream, mass.data_ptr(), width, k_pool.data_ptr(), v_pool.data_ptr(),
+         desc, block_tables.data_ptr(), blocks, context_lens.data_ptr(), budgets.data_ptr(),
+         int(sink), int(recent), _ptr(new_tables), new_blocks, kept.data_ptr(), keep,
+         new_lens.data_ptr(), mass_out.data_ptr(), mass_out.shape[2], seqs)
+    return kept, new_lens, mass_out
+
+
+def pa_compact_tokens(k_pool, v_pool, block_tables, kept, counts, base=None, new_tables=None,
+                      stream=None) -> None:
+    """Move K and V of row ``base[s] + kept[s][g][i]`` to row ``base[s] + i`` for every
+    sequence, KV head and i < ``counts[s]`` (int32 [S]), in place or into the blocks of
+    ``new_tables``.  ``kept``: int32 [S, Hkv, K], or [S, 1, K] for all heads alike,
+    ascending in i; ``base``: int32 [S] or None (zeros)."""
+    torch = _torch()
+    dev = k_pool.device
+    i32 = torch.int32
+    _arg("counts", counts, i32, dev)
+    desc, seqs, blocks = _batch_args(k_pool, block_tables, counts, dev)
+    _arg("v_pool", v_pool, torch.bfloat16, dev, k_pool.shape)
+    _arg("kept", kept, i32, dev)
+    _dims("kept", kept, 3)
+    if kept.shape[0] != seqs:
+        raise ValueError(f"kept must have {seqs} rows, got {kept.shape[0]}")
+    if base is not None:
+        _arg("base", base, i32, dev, (seqs,))
+    new_blocks = 0
+    if new_tables is not None:
+        _arg("new_tables", new_tables, i32, dev)
+        _dims("new_tables", new_tables, 2)
+        if new_tables.shape[0] != seqs:
+            raise ValueError(f"new_tables must have {seqs} rows, got {new_tables.shape[0]}")
+        new_blocks = new_tables.shape[1]
+    _run("pa_compact_tokens", dev, stream, k_pool.data_ptr(), v_pool.data_ptr(), desc,
+         block_tables.data_ptr(), blocks, _ptr(new_tables), new_blocks, _ptr(base),
+         kept.data_ptr(), kept.shape[1], kept.shape[2], counts.data_ptr(), seqs)

@@ -109,6 +109,13 @@ SIGNATURES = {
     "pa_tree_attention": (c_int, [c_vp, c_i64, c_vp, c_i32, c_i32, c_vp, c_i32, c_vp, c_vp,
                                   PoolDesc, c_vp, c_i32, c_vp, c_i32, c_i32, c_f32, c_vp, c_vp,
                                   c_vp, c_size, c_vp]),
+    # eviction (include/pa_evict.h)
+    "pa_attention_mass": (c_int, [c_vp, c_i64, c_vp, c_vp, c_i32, c_i32, c_vp, PoolDesc, c_vp, c_i32,
+                                  c_vp, c_i32, c_i32, c_f32, c_vp, c_vp, c_i64, c_vp]),
+    "pa_evict": (c_int, [c_vp, c_i64, c_vp, c_vp, PoolDesc, c_vp, c_i32, c_vp, c_vp, c_i32, c_i32,
+                         c_vp, c_i32, c_vp, c_i32, c_vp, c_vp, c_i64, c_i32, c_vp]),
+    "pa_compact_tokens": (c_int, [c_vp, c_vp, PoolDesc, c_vp, c_i32, c_vp, c_i32, c_vp, c_vp, c_i32,
+                                  c_i32, c_vp, c_i32, c_vp]),
     # paged read-bandwidth probe (include/pa_probe.h)
     "pa_read_probe": (c_int, [c_vp, c_vp, PoolDesc, c_vp, c_i32, c_vp, c_i32, c_vp, c_i32, c_vp]),
 }

@@ -1,0 +1,66 @@
+// Helpers shared by the kernels that walk a line of key tiles (tree attention,
+// accumulated attention weight).
+#pragma once
+
+#include "tc_common.cuh"
+
+namespace pa {
+
+__device__ __forceinline__ int ld_i32(const int32_t* ptr) {
+  int x;
+  asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(x) : "l"(ptr));
+  return x;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// One lane of a converged warp, always the same.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
+// A wait of a unit ring: several times as long as the waits for data, and heeding
+// no abort flag (every role takes every unit).
+__device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity, unsigned* err) {
+  for (int i = 0; i < 8; ++i)
+    if (mbar_wait(bar, parity, nullptr, err)) return true;
+  return false;
+}
+
+// A sequence of the batch, as the lengths on the device describe it.
+struct SeqRaw {
+  int q0, q1, L;
+};
+
+// Exclusive scan of one number per thread over a CTA of `warps` warps (`slots`: as
+// many words of shared memory); `total` is the sum of all.
+template <int kWarps>
+__device__ __forceinline__ long long cta_scan(long long mine, long long* slots, long long& total) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  long long scan = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, scan, o);
+    if (lane >= o) scan += v;
+  }
+  if (lane == 31) slots[warp] = scan;
+  __syncthreads();
+  long long before = scan - mine;
+  total = 0;
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += slots[w];
+    total += slots[w];
+  }
+  return before;
+}
+
+}  // namespace pa

@@ -1,0 +1,591 @@
+// Eviction: choosing the heaviest cached tokens of every KV head and packing
+// them.
+//
+// Choice (evict_select_kernel, one CTA per (sequence, head)): the weights become
+// unsigned keys of the same order and stay in registers (up to 32 per thread);
+// the key of the last token that fits is found bit by bit from the top -- a
+// candidate threshold, a count of the keys at or above it, one barrier -- until
+// a count hits the wanted number exactly or the bits run out.  Then every token
+// above the threshold is kept, and of those at it the lowest indices.  A warp
+// owns a run of tokens, so counts of ballots give each kept token its place in
+// order without sorting.  Longer rows (evict_select_long_kernel) do the same
+// over the row in memory, eight bits at a time with a histogram per warp.
+//
+// Move (compact): rows of 16-byte chunks.  Into fresh blocks all rows move at
+// once; in place a CTA takes one slice of the columns of one (sequence, head),
+// K or V, and goes through its rows in order, a chunk of rows read before it is
+// written: sources are never below their destinations, so a chunk's writes can
+// only hit rows that were read.
+//
+// Bound: HBM for the move (each kept row read and written once); the choice is
+// bound by its steps' latency.
+#include <algorithm>
+
+#include "../../include/pa_evict.h"
+#include "common.cuh"
+#include "internal.h"
+
+namespace pa {
+namespace {
+
+// ---------------------------------------------------------------------------
+// Choice
+// ---------------------------------------------------------------------------
+constexpr int kSelThreads = 1024;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelMost = 32;  // tokens per thread in registers: up to 32768 a row
+
+struct SelectParams {
+  const float* mass;
+  int64_t mass_stride;
+  const int32_t* context_lens;
+  const int32_t* budgets;
+  int sink, recent;
+  int32_t* kept;
+  int kept_stride;
+  int32_t* new_lens;
+  float* mass_out;
+  int64_t mass_out_stride;
+  int hkv;
+  int most_len;   // tokens of a table
+  unsigned int* err;
+};
+
+// What a row keeps: [0, sink) and [len - recent, len) whatever their weight, and
+// `need` of the tokens between.
+struct Choice {
+  int len, keep, sink, recent, need;
+};
+
+__device__ __forceinline__ Choice choice_of(const SelectParams& p, int s, bool flag) {
+  Choice c;
+  c.len = p.context_lens[s];
+  if (c.len < 0 || c.len > p.most_len || c.len > p.mass_stride) {
+    if (flag) raise_error(p.err, PA_DEV_ERR_CONTEXT);
+    c.len = 0;
+  }
+  const int64_t most = min(static_cast<int64_t>(p.kept_stride), p.mass_out_stride);
+  c.keep = max(0, min(c.len, p.budgets[s]));
+  if (c.keep > most) c.keep = static_cast<int>(most);
+  c.sink = min(p.sink, c.keep);
+  c.recent = min(p.recent, c.keep - c.sink);
+  c.need = c.keep - c.sink - c.recent;
+  return c;
+}
+
+// Keys in the order of the weights: NaN is the least (0), both zeros are alike.
+// On the bits alone: comparisons of floats would take denormal weights for zeros.
+__device__ __forceinline__ uint32_t key_of(float x) {
+  const uint32_t b = __float_as_uint(x), size = b & 0x7fffffffu;
+  if (size > 0x7f800000u) return 0;
+  if (size == 0) return 0x80000000u;
+  return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float weight_of(uint32_t key) {
+  if (key == 0) return __uint_as_float(0x7fc00000u);
+  return __uint_as_float((key & 0x80000000u) ? key & 0x7fffffffu : ~key);
+}
+
+// Sum over the CTA of one number per thread; `slots` alternates between two
+// arrays so that one barrier is enough.
+__device__ __forceinline__ int cta_sum(int x, int* slots, int warp, int lane) {
+  const int w = __reduce_add_sync(0xffffffffu, x);
+  if (lane == 0) slots[warp] = w;
+  __syncthreads();
+  return __reduce_add_sync(0xffffffffu, slots[lane]);
+}
+
+// Where this warp's kept tokens and ties begin: sums over the warps before it.
+__device__ __forceinline__ int2 warps_before(int2 x, int2* slots, int warp, int lane) {
+  if (lane == 0) slots[warp] = x;
+  __syncthreads();
+  const int2 v = slots[lane];
+  return make_int2(__reduce_add_sync(0xffffffffu, lane < warp ? v.x : 0),
+                   __reduce_add_sync(0xffffffffu, lane < warp ? v.y : 0));
+}
+
+// The kept tokens of a row, in order, from per-thread flags of one token each
+// (`sure`: forced or above the threshold; `at`: at it), for tokens that follow
+// one another along the lanes.  place and tie are the warp's running counts: kept
+// tokens, and ties, before these.
+__device__ __forceinline__ int place_of(bool sure, bool at, int ties, int lane, int& place,
+                                        int& tie) {
+  const uint32_t below = (1u << lane) - 1u;
+  const uint32_t ats = __ballot_sync(0xffffffffu, at);
+  const bool keep = sure || (at && tie + __popc(ats & below) < ties);
+  const uint32_t keeps = __ballot_sync(0xffffffffu, keep);
+  const int i = place + __popc(keeps & below);
+  place += __popc(keeps);
+  tie += __popc(ats);
+  return keep ? i : -1;
+}
+
+// ITEMS: tokens per lane at most.  Lane l's item k of warp w is token
+// (w * items + k) * 32 + l, items = ceil(len / 1024).
+template <int ITEMS>
+__global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(
+    const __grid_constant__ SelectParams p) {
+  __shared__ int sums[2][kSelWarps];
+  __shared__ int2 bases[kSelWarps];
+  // the move may be set up now (it waits for this grid's end)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int row = blockIdx.x;
+  const int s = row / p.hkv;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const Choice c = choice_of(p, s, row % p.hkv == 0 && tid == 0);
+  if (row % p.hkv == 0 && tid == 0) p.new_lens[s] = c.keep;
+  if (c.keep == 0) return;
+  const float* mass = p.mass + row * p.mass_stride;
+  const int items = (c.len + kSelThreads - 1) / kSelThreads;
+  const int first = warp * items * 32 + lane;
+  const int lo = c.sink, hi = c.len - c.recent;  // the tokens with a choice
+  uint32_t key[ITEMS];
+  uint32_t open = 0, forced = 0;  // bit k: item k has a choice, is kept anyway
+#pragma unroll
+  for (int k = 0; k < ITEMS; ++k) {
+    const int t = first + 32 * k;
+    const bool live = k < items && t < c.len;
+    key[k] = live ? key_of(mass[t]) : 0u;
+    if (live && t >= lo && t < hi && c.need > 0) open |= 1u << k;
+    if (live && (t < lo || t >= hi)) forced |= 1u << k;
+  }
+  // The largest threshold that at least `need` keys reach.
+  uint32_t bar = 0;
+  int above = hi - lo;  // keys at or above the threshold (0: all with a choice)
+  if (c.need > 0 && c.need < hi - lo) {
+    for (int b = 31; b >= 0 && above != c.need; --b) {
+      const uint32_t cand = bar | (1u << b);
+      uint32_t m = 0;
+#pragma unroll
+      for (int k = 0; k < ITEMS; ++k) m |= key[k] >= cand ? 1u << k : 0u;
+      const int n = cta_sum(__popc(m & open), sums[b & 1], warp, lane);
+      if (n >= c.need) {
+        bar = cand;
+        above = n;
+      }
+    }
+  }
+  // Above the threshold: kept; at it: the first ones in order, as many as fit.
+  uint32_t sure = forced, at = 0;
+#pragma unroll
+  for (int k = 0; k < ITEMS; ++k) {
+    if (key[k] > bar) sure |= open & (1u << k);
+    if (key[k] == bar) at |= open & (1u << k);
+  }
+  const int2 mine = make_int2(__reduce_add_sync(0xffffffffu, __popc(sure)),
+                              __reduce_add_sync(0xffffffffu, __popc(at)));
+  const int2 before = warps_before(mine, bases, warp, lane);
+  const int ties = c.keep - cta_sum(lane == 0 ? mine.x : 0, sums[0], warp, lane);
+  int place = before.x + min(before.y, ties), tie = before.y;
+  int32_t* kept = p.kept + static_cast<int64_t>(row) * p.kept_stride;
+  float* out = p.mass_out + row * p.mass_out_stride;
+#pragma unroll
+  for (int k = 0; k < ITEMS; ++k) {
+    if (k < items) {
+      const int i = place_of((sure >> k) & 1u, (at >> k) & 1u, ties, lane, place, tie);
+      if (i >= 0) {
+        kept[i] = first + 32 * k;
+        out[i] = weight_of(key[k]);  // (all weights were read before the last barrier)
+      }
+    }
+  }
+}
+
+// Rows of any length: token k * 1024 + tid is thread tid's in turn k.
+__global__ void __launch_bounds__(kSelThreads, 1) evict_select_long_kernel(
+    const __grid_constant__ SelectParams p) {
+  __shared__ int hist[kSelWarps][256];
+  __shared__ int2 bases[2][kSelWarps];
+  __shared__ uint32_t found[2];  // the digit, what is still needed within it
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int row = blockIdx.x;
+  const int s = row / p.hkv;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const Choice c = choice_of(p, s, row % p.hkv == 0 && tid == 0);
+  if (row % p.hkv == 0 && tid == 0) p.new_lens[s] = c.keep;
+  if (c.keep == 0) return;
+  const float* mass = p.mass + row * p.mass_stride;
+  const int lo = c.sink, hi = c.len - c.recent;
+  uint32_t bar = 0;
+  int rem = c.need;  // still needed among the keys that share the digits so far
+  if (c.need > 0 && c.need < hi - lo) {
+    for (int shift = 24; shift >= 0; shift -= 8) {
+      for (int i = tid; i < kSelWarps * 256; i += kSelThreads) (&hist[0][0])[i] = 0;
+      __syncthreads();
+#pragma unroll 4
+      for (int t = lo + tid; t < hi; t += kSelThreads) {
+        const uint32_t k = key_of(mass[t]);
+        if (shift == 24 || (k >> (shift + 8)) == (bar >> (shift + 8)))
+          atomicAdd(&hist[warp][(k >> shift) & 255u], 1);
+      }
+      __syncthreads();
+      if (tid < 256) {
+        int n = 0;
+        for (int w = 0; w < kSelWarps; ++w) n += hist[w][tid];
+        hist[0][tid] = n;
+      }
+      __syncthreads();
+      if (warp == 0) {
+        // lane l: digits 255 - 8 l down to 248 - 8 l
+        int n = 0;
+        for (int j = 0; j < 8; ++j) n += hist[0][255 - 8 * lane - j];
+        int upto = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += v;
+        }
+        int over = upto - n;  // keys of larger digits
+        if (over < rem && upto >= rem) {
+          for (int j = 0; j < 8; ++j) {
+            const int d = 255 - 8 * lane - j, h = hist[0][d];
+            if (over + h >= rem) {
+              found[0] = d;
+              found[1] = rem - over;
+              break;
+            }
+            over += h;
+          }
+        }
+      }
+      __syncthreads();
+      bar |= found[0] << shift;
+      rem = static_cast<int>(found[1]);
+    }
+  }
+  // Ties that fit: what the tokens surely kept leave of keep.
+  int n_sure = 0;
+  for (int t = lo + tid; t < hi; t += kSelThreads) n_sure += c.need > 0 && key_of(mass[t]) > bar;
+  __syncthreads();
+  n_sure = cta_sum(n_sure, hist[0], warp, lane);
+  const int ties = c.need - n_sure;
+  int32_t* kept = p.kept + static_cast<int64_t>(row) * p.kept_stride;
+  float* out = p.mass_out + row * p.mass_out_stride;
+  int done = 0, ties_done = 0;  // before this turn
+  for (int t0 = 0, turn = 0; t0 < c.len; t0 += kSelThreads, ++turn) {
+    const int t = t0 + tid;
+    const uint32_t k = t < c.len ? key_of(mass[t]) : 0u;
+    const bool open = t >= lo && t < hi && c.need > 0;
+    const bool sure = t < c.len && (t < lo || t >= hi || (open && k > bar));
+    const bool at = open && k == bar;
+    const int2 mine = make_int2(__popc(__ballot_sync(0xffffffffu, sure)),
+                                __popc(__ballot_sync(0xffffffffu, at)));
+    int2* slots = bases[turn & 1];
+    const int2 before = warps_before(mine, slots, warp, lane);
+    int tie = ties_done + before.y;
+    int place = done + before.x + min(tie, ties);
+    const int i = place_of(sure, at, ties, lane, place, tie);
+    if (i >= 0) {  // (i <= t: this turn's weights are read, later ones lie beyond)
+      kept[i] = t;
+      out[i] = weight_of(k);
+    }
+    const int2 v = slots[lane];
+    done += __reduce_add_sync(0xffffffffu, v.x);
+    ties_done += __reduce_add_sync(0xffffffffu, v.y);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Move
+// ---------------------------------------------------------------------------
+struct MoveParams {
+  uint4* k_pool;
+  uint4* v_pool;
+  int num_blocks, hkv;
+  const int32_t* tables;
+  int max_blocks;
+  const int32_t* new_tables;
+  int new_max_blocks;
+  const int32_t* base;
+  const int32_t* kept;
+  int64_t kept_seq, kept_head;  // strides
+  int kept_stride;
+  const int32_t* counts;
+  int num_seqs;
+  int parts;  // CTAs per (sequence, head)
+  unsigned int* err;
+};
+
+// Flat pool row of a sequence's row `pos` for KV head g, or -1.
+__device__ __forceinline__ int64_t pool_row(const MoveParams& p, const int32_t* table, int blocks,
+                                            int64_t pos, int g) {
+  if (pos < 0 || pos >= static_cast<int64_t>(blocks) * 16) {
+    raise_error(p.err, PA_DEV_ERR_CONTEXT);
+    return -1;
+  }
+  const int b = table[pos >> 4];
+  if (b < 0 || b >= p.num_blocks) {
+    raise_error(p.err, PA_DEV_ERR_BLOCK_ID);
+    return -1;
+  }
+  return (static_cast<int64_t>(b) * p.hkv + g) * 16 + (pos & 15);
+}
+
+__device__ __forceinline__ int move_count(const MoveParams& p, int s, bool flag) {
+  const int n = p.counts[s];
+  if (n >= 0 && n <= p.kept_stride) return n;
+  if (flag) raise_error(p.err, PA_DEV_ERR_CONTEXT);
+  return n < 0 ? 0 : p.kept_stride;
+}
+
+// Into other blocks: a warp takes eight rows; lanes 0-7 look the rows up, then
+// every row's K and V go as 16-byte chunks, a quarter (D = 64: a half) of the
+// warp's rows in flight at a time.
+constexpr int kMoveThreads = 256;
+constexpr int kMoveRows = 8;                                   // rows of a warp
+constexpr int kMoveCtaRows = kMoveRows * (kMoveThreads / 32);  // of a CTA's turn
+
+template <int D>
+__global__ void __launch_bounds__(kMoveThreads) move_out_kernel(const __grid_constant__ MoveParams p) {
+  constexpr int kLanes = D / 8;           // chunks of a row
+  constexpr int kAtOnce = 32 / kLanes;    // rows a warp covers with one access
+  constexpr int kSteps = kMoveRows / kAtOnce;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int sg = blockIdx.x / p.parts, part = blockIdx.x % p.parts;
+  const int s = sg / p.hkv, g = sg % p.hkv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n = move_count(p, s, g == 0 && part == 0 && threadIdx.x == 0);
+  const int base = p.base ? p.base[s] : 0;
+  const int32_t* kept = p.kept + s * p.kept_seq + g * p.kept_head;
+  const int32_t* table = p.tables + static_cast<int64_t>(s) * p.max_blocks;
+  const int32_t* new_table = p.new_tables + static_cast<int64_t>(s) * p.new_max_blocks;
+  for (int i0 = part * kMoveCtaRows + warp * kMoveRows; i0 < n; i0 += p.parts * kMoveCtaRows) {
+    int64_t src = -1, dst = -1;
+    const int i = i0 + lane;
+    if (lane < kMoveRows && i < n) {
+      src = pool_row(p, table, p.max_blocks, static_cast<int64_t>(base) + kept[i], g);
+      dst = pool_row(p, new_table, p.new_max_blocks, static_cast<int64_t>(base) + i, g);
+      if (src < 0 || dst < 0) src = dst = -1;
+    }
+    uint4 k[kSteps], v[kSteps];
+    int64_t to[kSteps];
+#pragma unroll
+    for (int j = 0; j < kSteps; ++j) {
+      const int r = j * kAtOnce + lane / kLanes;
+      const int64_t from = __shfl_sync(0xffffffffu, src, r);
+      to[j] = __shfl_sync(0xffffffffu, dst, r);
+      if (from >= 0) {
+        k[j] = p.k_pool[from * kLanes + lane % kLanes];
+        v[j] = p.v_pool[from * kLanes + lane % kLanes];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kSteps; ++j)
+      if (to[j] >= 0) {
+        p.k_pool[to[j] * kLanes + lane % kLanes] = k[j];
+        p.v_pool[to[j] * kLanes + lane % kLanes] = v[j];
+      }
+  }
+}
+
+// In place: blockIdx.x = ((sequence, head), slice); a slice is four 16-byte
+// chunks of K's or V's rows.  Thread i of a turn takes rows i / 4, + 64, ...
+constexpr int kSliceLanes = 4;
+constexpr int kPlaceUnroll = 4;
+
+template <int D>
+__global__ void __launch_bounds__(kMoveThreads) move_in_place_kernel(
+    const __grid_constant__ MoveParams p) {
+  constexpr int kRowChunks = D / 8;
+  constexpr int kSlices = kRowChunks / kSliceLanes;  // of K, and as many of V
+  constexpr int kRows = kMoveThreads / kSliceLanes;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int sg = blockIdx.x / (2 * kSlices), slice = blockIdx.x % (2 * kSlices);
+  const int s = sg / p.hkv, g = sg % p.hkv;
+  const int n = move_count(p, s, g == 0 && slice == 0 && threadIdx.x == 0);
+  const int base = p.base ? p.base[s] : 0;
+  const int32_t* kept = p.kept + s * p.kept_seq + g * p.kept_head;
+  const int32_t* table = p.tables + static_cast<int64_t>(s) * p.max_blocks;
+  uint4* pool = (slice < kSlices ? p.k_pool : p.v_pool) + (slice % kSlices) * kSliceLanes +
+                threadIdx.x % kSliceLanes;
+  const int r = threadIdx.x / kSliceLanes;
+  for (int i0 = 0; i0 < n; i0 += kRows * kPlaceUnroll) {
+    uint4 x[kPlaceUnroll];
+    int64_t to[kPlaceUnroll];
+#pragma unroll
+    for (int u = 0; u < kPlaceUnroll; ++u) {
+      const int i = i0 + u * kRows + r;
+      to[u] = -1;
+      if (i < n) {
+        const int t = kept[i];
+        if (t != i) {  // a token that stays is not touched
+          const int64_t from = pool_row(p, table, p.max_blocks, static_cast<int64_t>(base) + t, g);
+          to[u] = pool_row(p, table, p.max_blocks, static_cast<int64_t>(base) + i, g);
+          if (from < 0) to[u] = -1;
+          if (to[u] >= 0) x[u] = pool[from * kRowChunks];
+        }
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kPlaceUnroll; ++u)
+      if (to[u] >= 0) pool[to[u] * kRowChunks] = x[u];
+  }
+}
+
+template <typename F>
+int launch_dependent(F kernel, int grid, int threads, const MoveParams& p, bool dependent,
+                     cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = dependent ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) {
+    cudaGetLastError();
+    return PA_ERR_CUDA;
+  }
+  return PA_OK;
+}
+
+// `dependent`: the kernel before is the choice, whose end the move waits for
+// itself.
+int run_move(MoveParams& p, int head_dim, bool dependent, cudaStream_t stream) {
+  const int64_t rows = static_cast<int64_t>(p.num_seqs) * p.hkv;
+  if (p.new_tables) {
+    // enough CTAs to fill the device several times over, no more than the rows need
+    const int64_t most = (p.kept_stride + kMoveCtaRows - 1) / kMoveCtaRows;
+    const int64_t want = (static_cast<int64_t>(num_sms()) * 64 + rows - 1) / rows;
+    p.parts = static_cast<int>(std::max<int64_t>(1, std::min(most, want)));
+    if (rows * p.parts > 0x7fffffff) return PA_ERR_UNSUPPORTED;
+    const int grid = static_cast<int>(rows * p.parts);
+    return head_dim == 128
+               ? launch_dependent(move_out_kernel<128>, grid, kMoveThreads, p, dependent, stream)
+               : launch_dependent(move_out_kernel<64>, grid, kMoveThreads, p, dependent, stream);
+  }
+  const int64_t grid = rows * 2 * (head_dim / 8 / kSliceLanes);
+  if (grid > 0x7fffffff) return PA_ERR_UNSUPPORTED;
+  return head_dim == 128
+             ? launch_dependent(move_in_place_kernel<128>, static_cast<int>(grid), kMoveThreads, p,
+                                dependent, stream)
+             : launch_dependent(move_in_place_kernel<64>, static_cast<int>(grid), kMoveThreads, p,
+                                dependent, stream);
+}
+
+template <int ITEMS>
+int launch_select(const SelectParams& p, int rows, cudaStream_t stream) {
+  evict_select_kernel<ITEMS><<<rows, kSelThreads, 0, stream>>>(p);
+  return launch_status();
+}
+
+// Tokens of a table, an int.
+int64_t table_tokens(int max_blocks) { return static_cast<int64_t>(max_blocks) * 16; }
+
+}  // namespace
+}  // namespace pa
+
+using namespace pa;
+
+extern "C" {
+
+int pa_evict(const float* mass, int64_t mass_stride, void* k_pool, void* v_pool, pa_pool_desc pool,
+             const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* context_lens,
+             const int32_t* budgets, int32_t sink, int32_t recent, const int32_t* new_tables,
+             int32_t new_max_blocks, int32_t* kept, int32_t kept_stride, int32_t* new_lens,
+             float* mass_out, int64_t mass_out_stride, int32_t num_seqs, void* stream) {
+  PA_NVTX_RANGE("pa_evict");
+  int st = check_pool(pool);
+  if (st != PA_OK) return st;
+  if (num_seqs < 0 || max_blocks_per_seq <= 0 || sink < 0 || recent < 0 || kept_stride < 0 ||
+      mass_stride < 0 || mass_out_stride < 0)
+    return PA_ERR_ARG;
+  if (num_seqs == 0) return PA_OK;
+  if (!mass || !k_pool || !v_pool || !block_tables || !context_lens || !budgets || !kept ||
+      !new_lens || !mass_out || new_lens == context_lens)
+    return PA_ERR_ARG;
+  if (!aligned16(k_pool) || !aligned16(v_pool)) return PA_ERR_ARG;
+  if (new_tables && (new_max_blocks <= 0 || new_tables == block_tables)) return PA_ERR_ARG;
+  if (mass_out == mass && mass_out_stride != mass_stride) return PA_ERR_ARG;
+  const int64_t rows = static_cast<int64_t>(num_seqs) * pool.num_kv_heads;
+  if (rows > 0x7fffffff || table_tokens(max_blocks_per_seq) > (1 << 30)) return PA_ERR_UNSUPPORTED;
+  SelectParams p = {};
+  p.err = device_error_word();
+  if (!p.err) return PA_ERR_CUDA;
+  p.mass = mass;
+  p.mass_stride = mass_stride;
+  p.context_lens = context_lens;
+  p.budgets = budgets;
+  p.sink = sink;
+  p.recent = recent;
+  p.kept = kept;
+  p.kept_stride = kept_stride;
+  p.new_lens = new_lens;
+  p.mass_out = mass_out;
+  p.mass_out_stride = mass_out_stride;
+  p.hkv = pool.num_kv_heads;
+  p.most_len = static_cast<int>(table_tokens(max_blocks_per_seq));
+  // the longest row there can be decides how many tokens a thread holds
+  const int64_t longest = std::min<int64_t>(p.most_len, mass_stride);
+  const int r = static_cast<int>(rows);
+  if (longest <= 4 * kSelThreads)
+    st = launch_select<4>(p, r, as_stream(stream));
+  else if (longest <= 8 * kSelThreads)
+    st = launch_select<8>(p, r, as_stream(stream));
+  else if (longest <= 16 * kSelThreads)
+    st = launch_select<16>(p, r, as_stream(stream));
+  else if (longest <= kSelMost * kSelThreads)
+    st = launch_select<kSelMost>(p, r, as_stream(stream));
+  else {
+    evict_select_long_kernel<<<r, kSelThreads, 0, as_stream(stream)>>>(p);
+    st = launch_status();
+  }
+  if (st != PA_OK || kept_stride == 0) return st;
+  MoveParams m = {};
+  m.k_pool = static_cast<uint4*>(k_pool);
+  m.v_pool = static_cast<uint4*>(v_pool);
+  m.num_blocks = pool.num_blocks;
+  m.hkv = pool.num_kv_heads;
+  m.tables = block_tables;
+  m.max_blocks = max_blocks_per_seq;
+  m.new_tables = new_tables;
+  m.new_max_blocks = new_max_blocks;
+  m.kept = kept;
+  m.kept_head = kept_stride;
+  m.kept_seq = static_cast<int64_t>(kept_stride) * pool.num_kv_heads;
+  m.kept_stride = kept_stride;
+  m.counts = new_lens;
+  m.num_seqs = num_seqs;
+  m.err = p.err;
+  return run_move(m, pool.head_dim, true, as_stream(stream));
+}
+
+int pa_compact_tokens(void* k_pool, void* v_pool, pa_pool_desc pool, const int32_t* block_tables,
+                      int32_t max_blocks_per_seq, const int32_t* new_tables,
+                      int32_t new_max_blocks, const int32_t* base, const int32_t* kept,
+                      int32_t kept_heads, int32_t kept_stride, const int32_t* counts,
+                      int32_t num_seqs, void* stream) {
+  PA_NVTX_RANGE("pa_compact_tokens");
+  const int st = check_pool(pool);
+  if (st != PA_OK) return st;
+  if (num_seqs < 0 || max_blocks_per_seq <= 0 || kept_stride < 0) return PA_ERR_ARG;
+  if (kept_heads != 1 && kept_heads != pool.num_kv_heads) return PA_ERR_SHAPE;
+  if (num_seqs == 0 || kept_stride == 0) return PA_OK;
+  if (!k_pool || !v_pool || !block_tables || !kept || !counts) return PA_ERR_ARG;
+  if (!aligned16(k_pool) || !aligned16(v_pool)) return PA_ERR_ARG;
+  if (new_tables && (new_max_blocks <= 0 || new_tables == block_tables)) return PA_ERR_ARG;
+  MoveParams m = {};
+  m.err = device_error_word();
+  if (!m.err) return PA_ERR_CUDA;
+  m.k_pool = static_cast<uint4*>(k_pool);
+  m.v_pool = static_cast<uint4*>(v_pool);
+  m.num_blocks = pool.num_blocks;
+  m.hkv = pool.num_kv_heads;
+  m.tables = block_tables;
+  m.max_blocks = max_blocks_per_seq;
+  m.new_tables = new_tables;
+  m.new_max_blocks = new_max_blocks;
+  m.base = base;
+  m.kept = kept;
+  m.kept_head = kept_heads == 1 ? 0 : kept_stride;
+  m.kept_seq = static_cast<int64_t>(kept_stride) * kept_heads;
+  m.kept_stride = kept_stride;
+  m.counts = counts;
+  m.num_seqs = num_seqs;
+  return run_move(m, pool.head_dim, false, as_stream(stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,609 @@
+// Attention weight that a step's queries give every cached token, on the
+// 5th-generation tensor cores.
+//
+// For one KV head the rows (query, q head of the group) of a sequence are columns
+// here: floor(128/G) queries make a column tile, and per key tile of 128
+//     S^T [128 keys x columns] = K_tile . Q_tile^T      (D/16 MMAs, N = columns)
+// so a thread owns a key, and its weights
+//     sum over columns of 2^(scale' s - lse')           (both in log2 units)
+// never leave its registers until all column tiles are done: no atomics, no
+// exchange, and a fixed order of the sum.  The columns' lse' wait in shared memory
+// beside the q tile; a query before the key in the chunk drops out by its column
+// number.
+//
+// Work split: a key tile costs as many places as column tiles look at it (a
+// causal chunk's later keys are seen by fewer), and the places of all key tiles,
+// in order, are cut into equal stretches, one per CTA; a key tile belongs to the
+// stretch that holds its first place.  A unit is up to four neighbouring key
+// tiles, which share each column tile's load: their K tiles stay in shared memory
+// while the q tiles stream by, and each has its own scores in tensor memory and
+// its own warpgroup.
+//
+// Bound: HBM for a few queries (K once); for many the exponentials (128 keys x
+// 128 columns are 1024 cycles of an SM's multi-function units, 512 of its tensor
+// cores).
+//
+// Roles (one CTA per SM): warp 0 copies K, warp 1 issues the MMAs, warp 2 copies q
+// and its lse, warp 3 walks the stretch and publishes units, warps 4-19 are the
+// four warpgroups.  Every wait is bounded.
+#include <math_constants.h>
+
+#include "../../include/pa_evict.h"
+#include "draft_common.cuh"
+#include "internal.h"
+
+namespace pa {
+namespace {
+
+using namespace tc;
+
+constexpr int kThreads = 640;
+constexpr int kRegion = 128 * 128;
+constexpr int kQSlots = 2;
+constexpr int kUnits = 4;
+constexpr int kUnitTiles = 4;          // key tiles of a unit at most
+constexpr int kUnitReaders = 3 + 16;   // K, MMA, q, warpgroup warps
+constexpr int kMaskRing = 16;
+constexpr uint32_t kTmemCols = 512;    // four tiles of scores
+
+template <int D>
+struct Cfg {
+  static constexpr int kHalves = D / 64;
+  static constexpr int kTileBytes = kHalves * kRegion;
+  static constexpr int kSlots = D == 128 ? 5 : 9;  // K ring
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffK = kQSlots * kTileBytes;
+  static constexpr int kOffLse = kOffK + kSlots * kTileBytes;  // [kQSlots][128]
+  static constexpr int kOffUnit = kOffLse + kQSlots * 128 * 4;
+  static constexpr int kOffBar = kOffUnit + kUnits * 32;
+  static constexpr int kNumBars = 2 * kQSlots + 2 * kSlots + 2 * kUnits + 2 * kUnitTiles + 1;
+  // tensor-memory slot, abort flag, plan {sequence, place in it (8 bytes)}
+  static constexpr int kOffMisc = kOffBar + kNumBars * 8;
+  static constexpr int kOffMask = kOffMisc + 24;
+  static constexpr int kOffScan = (kOffMask + 4 * kMaskRing + 7) / 8 * 8;
+  static constexpr int kSmem = kOffScan + kThreads / 32 * 8;
+  static_assert(kSmem <= 232448, "shared memory per CTA");
+};
+
+struct __align__(64) MassParams {
+  CUtensorMap tm_k;
+  CUtensorMap tm_q;
+  const float* lse;
+  const int32_t* cu_q;  // NULL: row s is sequence s's
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  const float* mass_in;
+  float* mass_out;
+  int64_t mass_stride;
+  unsigned int* err;
+  int total_q;
+  int max_n;
+  int max_blocks;
+  int num_blocks;
+  int hkv;
+  int hq;
+  int group;
+  int tpt;  // queries of a column tile
+  int num_seqs;
+  float scale_log2;
+};
+
+struct Seq {
+  int q0, n, L;
+  int tiles;  // 0: nothing to do
+  int cols;   // column tiles
+};
+
+__device__ __forceinline__ SeqRaw fetch_seq(const MassParams& p, int s) {
+  SeqRaw r;
+  r.q0 = p.cu_q ? ld_i32(p.cu_q + s) : s;
+  r.q1 = p.cu_q ? ld_i32(p.cu_q + s + 1) : s + 1;
+  r.L = ld_i32(p.context_lens + s);
+  return r;
+}
+
+// (A decode step's row belongs to an empty context too: nothing to do, no error.)
+__device__ __forceinline__ Seq decode_seq(const MassParams& p, const SeqRaw& r, unsigned* err) {
+  Seq q;
+  q.q0 = r.q0;
+  q.n = r.q1 - r.q0;
+  q.L = r.L;
+  q.tiles = q.cols = 0;
+  if (!p.cu_q && r.L == 0) return q;
+  const bool ok = r.q0 >= 0 && r.q1 >= r.q0 && r.q1 <= p.total_q && q.n <= p.max_n &&
+                  r.L >= q.n && r.L <= p.max_blocks * 16 && r.L <= p.mass_stride;
+  if (!ok && err) raise_error(err, PA_DEV_ERR_CONTEXT);
+  if (!ok || r.L == 0) return q;
+  q.tiles = (r.L + 127) >> 7;
+  q.cols = (q.n + p.tpt - 1) / p.tpt;
+  return q;
+}
+
+// Column tiles whose queries all lie before key tile j: they do not see it.
+__device__ __forceinline__ int first_cols(const Seq& q, int j, int tpt) {
+  const int rel = j * 128 - (q.L - q.n);
+  return rel <= 0 ? 0 : rel / tpt;
+}
+// Places of a key tile (one for a tile that no query of the step sees: its sums
+// are copied all the same) and of a head.
+__device__ __forceinline__ int tile_places(const Seq& q, int j, int tpt) {
+  return max(1, q.cols - first_cols(q, j, tpt));
+}
+// Key tiles that every column tile sees.
+__device__ __forceinline__ int full_tiles(const Seq& q, int tpt) {
+  return min(q.tiles, (q.L - q.n + tpt - 1) / 128 + 1);
+}
+__device__ __forceinline__ long long head_places(const Seq& q, int tpt) {
+  if (!q.tiles) return 0;
+  const int full = full_tiles(q, tpt);
+  long long sum = static_cast<long long>(full) * max(1, q.cols);
+  for (int j = full; j < q.tiles; ++j) sum += tile_places(q, j, tpt);
+  return sum;
+}
+
+// Key tiles [j0, j0 + nj) of one (sequence, head); nj 0: no more.
+struct __align__(16) UnitWords {
+  int s, g, q0, n;
+  int L, j0, nj, pad;
+};
+static_assert(sizeof(UnitWords) == 32, "two 16-byte words");
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_constant__ MassParams p) {
+  using C = Cfg<D>;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const uint32_t sbase = smem_u32(smem);
+  float* lse_s = reinterpret_cast<float*>(smem + C::kOffLse);
+  UnitWords* units = reinterpret_cast<UnitWords*>(smem + C::kOffUnit);
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  uint64_t* q_empty = q_full + kQSlots;
+  uint64_t* k_full = q_empty + kQSlots;
+  uint64_t* k_empty = k_full + C::kSlots;
+  uint64_t* u_full = k_empty + C::kSlots;
+  uint64_t* u_empty = u_full + kUnits;
+  uint64_t* s_full = u_empty + kUnits;        // per warpgroup: scores ready
+  uint64_t* s_free = s_full + kUnitTiles;     // and read
+  uint64_t* drain = s_free + kUnitTiles;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+  volatile int* plan_seq = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8);
+  volatile long long* plan_at = reinterpret_cast<volatile long long*>(smem + C::kOffMisc + 16);
+  volatile uint32_t* kmask = reinterpret_cast<volatile uint32_t*>(smem + C::kOffMask);
+  static_assert(C::kOffMisc % 8 == 0 && C::kOffUnit % 16 == 0, "alignment of the words");
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (sbase & 1023u) {  // the swizzled tiles need it, and the compiler gives it
+    if (tid == 0) raise_error(p.err, PA_DEV_ERR_TIMEOUT);
+    return;
+  }
+  if (tid == 0) {
+    for (int i = 0; i < kQSlots; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1 + 16);  // the MMAs, and every warpgroup warp (the lse)
+    }
+    for (int i = 0; i < C::kSlots; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < kUnits; ++i) {
+      mbar_init(&u_full[i], 1);
+      mbar_init(&u_empty[i], kUnitReaders);
+    }
+    for (int w = 0; w < kUnitTiles; ++w) {
+      mbar_init(&s_full[w], 1);
+      mbar_init(&s_free[w], 4);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    prefetch_tmap(&p.tm_k);
+    prefetch_tmap(&p.tm_q);
+  }
+  // Where this CTA's stretch begins: as in the tree kernel, a scan over the
+  // threads' runs of sequences.
+  long long chunk, total;
+  {
+    const int per = (p.num_seqs + kThreads - 1) / kThreads;
+    const int s_lo = min(tid * per, p.num_seqs), s_hi = min(s_lo + per, p.num_seqs);
+    long long mine = 0;
+    for (int s = s_lo; s < s_hi; ++s)
+      mine += p.hkv * head_places(decode_seq(p, fetch_seq(p, s), blockIdx.x == 0 ? p.err : nullptr),
+                                  p.tpt);
+    const long long before = cta_scan<kThreads / 32>(
+        mine, reinterpret_cast<long long*>(smem + C::kOffScan), total);
+    chunk = (total + gridDim.x - 1) / gridDim.x;
+    if (chunk < 1) chunk = 1;
+    const long long begin = chunk * blockIdx.x;
+    if (begin >= before && begin < before + mine) {
+      long long at = begin - before;
+      for (int s = s_lo; s < s_hi; ++s) {
+        const long long places =
+            p.hkv * head_places(decode_seq(p, fetch_seq(p, s), nullptr), p.tpt);
+        if (at < places) {
+          *plan_seq = s;
+          *plan_at = at;
+          break;
+        }
+        at -= places;
+      }
+    }
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, kTmemCols);
+  fence_barrier_init();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int rows_box = p.tpt * p.group;  // columns of a whole tile
+
+  uint32_t u_at = 0;
+  UnitWords u;
+  auto next_unit = [&]() -> bool {
+    const int slot = u_at % kUnits;
+    if (!ring_wait(&u_full[slot], (u_at / kUnits) & 1, p.err)) return false;
+    u = units[slot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&u_empty[slot]);
+    ++u_at;
+    return u.nj > 0;
+  };
+  auto unit_seq = [&]() {
+    Seq q;
+    q.q0 = u.q0;
+    q.n = u.n;
+    q.L = u.L;
+    q.tiles = (u.L + 127) >> 7;
+    q.cols = (u.n + p.tpt - 1) / p.tpt;
+    return q;
+  };
+
+  if (warp == 3) {
+    // ===================== the walk along the stretch =====================
+    const long long begin = chunk * blockIdx.x;
+    long long left = total - begin < chunk ? total - begin : chunk;  // places to the border
+    int s = 0, g = 0, j = 0;
+    Seq cur = {};
+    SeqRaw next = {};
+    auto enter = [&](const SeqRaw& r) {
+      cur = decode_seq(p, r, nullptr);
+      if (s + 1 < p.num_seqs) next = fetch_seq(p, s + 1);
+    };
+    auto next_head = [&]() {
+      j = 0;
+      if (++g < p.hkv) return;
+      g = 0;
+      while (s + 1 < p.num_seqs) {
+        const SeqRaw r = next;
+        ++s;
+        enter(r);
+        if (cur.tiles > 0) return;
+      }
+      left = 0;  // past the last sequence
+    };
+    if (left > 0) {
+      s = *plan_seq;
+      enter(fetch_seq(p, s));
+      const long long head = head_places(cur, p.tpt);
+      const long long in = *plan_at;
+      g = static_cast<int>(in / head);
+      long long at = in - g * head;  // the first tile whose first place is at or past this
+      const int each = max(1, cur.cols), full = full_tiles(cur, p.tpt);
+      const long long whole = min(static_cast<long long>(full), (at + each - 1) / each);
+      j = static_cast<int>(whole);
+      at -= whole * each;  // places before tile j that belong to the CTA before: at <= 0
+      while (at > 0 && j < cur.tiles) at -= tile_places(cur, j++, p.tpt);
+      left += at;  // the stretch begins -at places later
+      if (j >= cur.tiles) next_head();
+    }
+    while (true) {
+      UnitWords w = {};
+      if (left > 0) {
+        w.s = s;
+        w.g = g;
+        w.q0 = cur.q0;
+        w.n = cur.n;
+        w.L = cur.L;
+        w.j0 = j;
+        while (w.nj < kUnitTiles && j < cur.tiles && left > 0) {
+          left -= tile_places(cur, j, p.tpt);
+          ++w.nj;
+          ++j;
+        }
+        if (j == cur.tiles && left > 0) next_head();
+      }
+      const int slot = u_at % kUnits;
+      if (!ring_wait(&u_empty[slot], ((u_at / kUnits) & 1) ^ 1, p.err)) break;
+      if (lane == 0) {
+        units[slot] = w;
+        mbar_arrive(&u_full[slot]);
+      }
+      __syncwarp();
+      ++u_at;
+      if (w.nj == 0) break;
+    }
+  } else if (warp == 0) {
+    // ============================ K producer ============================
+    uint32_t kt = 0, issued = 0;
+    while (next_unit()) {
+      const int32_t* table = p.block_tables + static_cast<int64_t>(u.s) * p.max_blocks;
+      const int blocks = (u.L + 15) >> 4;
+      const int b = u.j0 * 8 + lane;  // the unit's 32 entries at most
+      const int ent = b < blocks && lane < 8 * u.nj ? ld_i32(table + b) : -1;
+      for (int jj = 0; jj < u.nj; ++jj, ++kt) {
+        int pb = __shfl_sync(0xffffffffu, ent, jj * 8 + (lane & 7));
+        const bool wanted = lane < 8 && (u.j0 + jj) * 8 + lane < blocks;
+        if (wanted && (pb < 0 || pb >= p.num_blocks)) {
+          raise_error(p.err, PA_DEV_ERR_BLOCK_ID);
+          pb = -1;
+        }
+        const bool get = wanted && pb >= 0;
+        const unsigned vm = __ballot_sync(0xffffffffu, get);
+        const int slot = kt % C::kSlots;
+        mbar_wait(&k_empty[slot], ((kt / C::kSlots) & 1) ^ 1, abort_flag, p.err);
+        if (__any_sync(0xffffffffu, *abort_flag)) continue;
+        if (lane == 0) {
+          kmask[kt % kMaskRing] = vm;
+          mbar_arrive_expect_tx(&k_full[slot], __popc(vm) * C::kHalves * 2048);
+        }
+        __syncwarp();
+        if (get) {
+          const int row = (pb * p.hkv + u.g) * 16;
+          const uint32_t dst = sbase + C::kOffK + slot * C::kTileBytes + lane * 2048;
+          tma_load_2d(dst, &p.tm_k, 0, row, &k_full[slot]);
+          if (D == 128) tma_load_2d(dst + kRegion, &p.tm_k, 64, row, &k_full[slot]);
+        }
+        issued = kt + 1;
+      }
+    }
+    if (*abort_flag && lane == 0)
+      for (uint32_t w = issued > C::kSlots ? issued - C::kSlots : 0; w < issued; ++w)
+        mbar_wait(&k_full[w % C::kSlots], (w / C::kSlots) & 1, nullptr, p.err);
+  } else if (warp == 2) {
+    // =========================== q producer ===========================
+    uint32_t qi = 0, issued = 0;
+    while (next_unit()) {
+      const Seq q = unit_seq();
+      for (int i = first_cols(q, u.j0, p.tpt); i < q.cols; ++i, ++qi) {
+        const int qs = qi % kQSlots;
+        mbar_wait(&q_empty[qs], ((qi / kQSlots) & 1) ^ 1, abort_flag, p.err);
+        if (__any_sync(0xffffffffu, *abort_flag)) continue;
+        // column c: query i * tpt + c / G, head c % G; +inf: a column that adds nothing
+        const int cols = min(p.tpt, q.n - i * p.tpt) * p.group;
+        for (int c = lane; c < 128; c += 32) {
+          float e = CUDART_INF_F;
+          if (c < cols) {
+            const int64_t row = q.q0 + static_cast<int64_t>(i) * p.tpt + c / p.group;
+            e = __ldg(p.lse + row * p.hq + u.g * p.group + c % p.group);
+            e = e == -CUDART_INF_F ? CUDART_INF_F : e * kLog2e;
+          }
+          lse_s[qs * 128 + c] = e;
+        }
+        __syncwarp();
+        if (lane == 0) {
+          const uint32_t dst = sbase + C::kOffQ + qs * C::kTileBytes;
+          const int token = q.q0 + i * p.tpt;
+          mbar_arrive_expect_tx(&q_full[qs], C::kHalves * rows_box * 128);
+          tma_load_3d(dst, &p.tm_q, 0, u.g * p.group, token, &q_full[qs]);
+          if (D == 128) tma_load_3d(dst + kRegion, &p.tm_q, 64, u.g * p.group, token, &q_full[qs]);
+        }
+        issued = qi + 1;
+      }
+    }
+    if (*abort_flag && lane == 0)
+      for (uint32_t w = issued > kQSlots ? issued - kQSlots : 0; w < issued; ++w)
+        mbar_wait(&q_full[w % kQSlots], (w / kQSlots) & 1, nullptr, p.err);
+  } else if (warp == 1) {
+    // ============================= MMA ==============================
+    const uint32_t ubase = __shfl_sync(0xffffffffu, sbase, 0);
+    const uint32_t utmem = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint64_t dq0 = smem_desc_sw128(ubase + C::kOffQ, 16, 1024);
+    const uint64_t dk0 = smem_desc_sw128(ubase + C::kOffK, 16, 1024);
+    uint32_t qi = 0, kt0 = 0, steps[kUnitTiles] = {0, 0, 0, 0};
+    while (next_unit()) {
+      const Seq q = unit_seq();
+      const int nj = __shfl_sync(0xffffffffu, u.nj, 0);
+      const int i0 = first_cols(q, u.j0, p.tpt);
+      if (i0 >= q.cols)  // no query sees the unit: its K is passed over
+        for (int jj = 0; jj < nj; ++jj) {
+          const uint32_t kt = kt0 + jj;
+          mbar_wait(&k_full[kt % C::kSlots], (kt / C::kSlots) & 1, abort_flag, p.err);
+          if (lane == 0) mbar_arrive(&k_empty[kt % C::kSlots]);
+        }
+      for (int i = i0; i < q.cols; ++i, ++qi) {
+        const int qs = qi % kQSlots;
+        const int cols = min(p.tpt, q.n - i * p.tpt) * p.group;
+        const uint32_t idesc = idesc_bf16_f32(128, (cols + 15) & ~15, false, false);
+        const uint64_t qb = desc_add(dq0, qs * C::kTileBytes);
+        mbar_wait(&q_full[qs], (qi / kQSlots) & 1, abort_flag, p.err);
+#pragma unroll
+        for (int jj = 0; jj < kUnitTiles; ++jj) {
+          if (jj < nj) {
+            const uint32_t kt = kt0 + jj;
+            const int slot = kt % C::kSlots;
+            mbar_wait(&k_full[slot], (kt / C::kSlots) & 1, abort_flag, p.err);
+            mbar_wait(&s_free[jj], (steps[jj] & 1) ^ 1, abort_flag, p.err);
+            ++steps[jj];
+            tc_fence_after();
+            const uint64_t ka = desc_add(dk0, slot * C::kTileBytes);
+            if (!__any_sync(0xffffffffu, *abort_flag) && elect_one()) {
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k) {
+                const uint32_t off = (k >> 2) * kRegion + (k & 3) * 32;
+                umma_ss(utmem + 128 * jj, desc_add(ka, off), desc_add(qb, off), idesc,
+                        k > 0 ? 1u : 0u);
+              }
+              umma_commit(&s_full[jj]);
+              if (i == q.cols - 1) umma_commit(&k_empty[slot]);
+              if (jj == nj - 1) umma_commit(&q_empty[qs]);
+            }
+            __syncwarp();
+          }
+        }
+      }
+      kt0 += nj;
+    }
+    if (elect_one()) umma_commit(drain);
+    __syncwarp();
+    mbar_wait(drain, 0, nullptr, p.err);
+  } else {
+    // ====================== weights of a thread's key ======================
+    const int wg = (warp - 4) >> 2;  // key tile of the unit, scores in tensor memory
+    const int q4 = warp & 3;
+    const int r = q4 * 32 + lane;
+    const uint32_t scol = tmem + (static_cast<uint32_t>(q4 * 32) << 16) + 128 * wg;
+    const float sc = p.scale_log2;
+    uint32_t qi = 0, kt0 = 0, steps = 0;
+    while (next_unit()) {
+      const Seq q = unit_seq();
+      const int i0 = first_cols(q, u.j0, p.tpt);
+      if (wg >= u.nj) {  // no tile: only lets the q slots go, each in its turn
+        for (int i = i0; i < q.cols; ++i, ++qi) {
+          mbar_wait(&q_full[qi % kQSlots], (qi / kQSlots) & 1, abort_flag, p.err);
+          if (lane == 0) mbar_arrive(&q_empty[qi % kQSlots]);
+        }
+        kt0 += u.nj;
+        continue;
+      }
+      const int key = (u.j0 + wg) * 128 + r;
+      const int64_t at = (static_cast<int64_t>(u.s) * p.hkv + u.g) * p.mass_stride + key;
+      const float before = p.mass_in && key < q.L ? p.mass_in[at] : 0.f;
+      const int rel = key - (q.L - q.n);  // this key among the step's own tokens
+      float sum0 = 0.f, sum1 = 0.f;
+      for (int i = i0; i < q.cols; ++i, ++qi, ++steps) {
+        const int cols = min(p.tpt, q.n - i * p.tpt) * p.group;
+        const int from = max(0, rel - i * p.tpt) * p.group;  // columns that see the key
+        const float* e = lse_s + (qi % kQSlots) * 128;
+        mbar_wait(&s_full[wg], steps & 1, abort_flag, p.err);
+        tc_fence_after();
+#pragma unroll 1
+        for (int c0 = 0; c0 < cols; c0 += 16) {
+          float x[16];
+          tmem_ld16(scol + c0, x);
+#pragma unroll
+          for (int c = 0; c < 16; c += 4) {
+            const float4 l4 = *reinterpret_cast<const float4*>(e + c0 + c);
+            const float l[4] = {l4.x, l4.y, l4.z, l4.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int col = c0 + c + k;
+              const float y = col >= from && col < cols ? fmaf(x[c + k], sc, -l[k]) : -CUDART_INF_F;
+              if (k & 1)
+                sum1 += exp2f(y);
+              else
+                sum0 += exp2f(y);
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&s_free[wg]);
+          mbar_arrive(&q_empty[qi % kQSlots]);
+        }
+      }
+      // (a page that was not loaded: nothing added)
+      bool loaded = true;
+      if (i0 < q.cols) {
+        loaded = (kmask[(kt0 + wg) % kMaskRing] >> (r >> 4)) & 1u;
+      }
+      if (key < q.L) p.mass_out[at] = before + (loaded ? sum0 + sum1 : 0.f);
+      kt0 += u.nj;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int D>
+int launch_mass(MassParams& p, const void* q, int64_t q_stride, const void* k_pool,
+                const pa_pool_desc& pool, int64_t most_tiles, cudaStream_t stream) {
+  const int64_t rows = static_cast<int64_t>(pool.num_blocks) * pool.num_kv_heads * 16;
+  {
+    const uint64_t dims[2] = {static_cast<uint64_t>(D), static_cast<uint64_t>(rows)};
+    const uint64_t strides[1] = {D * 2};
+    const uint32_t box[2] = {64, 16};
+    if (!encode_bf16_map(&p.tm_k, k_pool, 2, dims, strides, box)) return PA_ERR_CUDA;
+  }
+  {
+    const uint64_t dims[3] = {static_cast<uint64_t>(D), static_cast<uint64_t>(p.hq),
+                              static_cast<uint64_t>(p.total_q)};
+    const uint64_t strides[2] = {D * 2, static_cast<uint64_t>(q_stride) * 2};
+    const uint32_t box[3] = {64, static_cast<uint32_t>(p.group), static_cast<uint32_t>(p.tpt)};
+    if (!encode_bf16_map(&p.tm_q, q, 3, dims, strides, box)) return PA_ERR_CUDA;
+  }
+  static KernelLaunchCache cache;
+  if (cache.blocks_per_sm(reinterpret_cast<const void*>(mass_tc_kernel<D>), kThreads,
+                          Cfg<D>::kSmem) < 1)
+    return PA_ERR_CUDA;
+  const int64_t sms = num_sms();
+  mass_tc_kernel<D><<<static_cast<int>(most_tiles < sms ? most_tiles : sms), kThreads,
+                      Cfg<D>::kSmem, stream>>>(p);
+  return launch_status();
+}
+
+}  // namespace
+}  // namespace pa
+
+using namespace pa;
+
+extern "C" {
+
+int pa_attention_mass(const void* q, int64_t q_stride, const float* lse, const int32_t* cu_q_lens,
+                      int32_t total_q, int32_t max_q_len, const void* k_pool, pa_pool_desc pool,
+                      const int32_t* block_tables, int32_t max_blocks_per_seq,
+                      const int32_t* context_lens, int32_t num_seqs, int32_t num_q_heads,
+                      float scale, const float* mass_in, float* mass_out, int64_t mass_stride,
+                      void* stream) {
+  PA_NVTX_RANGE("pa_attention_mass");
+  const int st = check_pool(pool);
+  if (st != PA_OK) return st;
+  if (num_seqs < 0 || total_q < 0 || num_q_heads <= 0 || max_blocks_per_seq <= 0 || mass_stride < 0)
+    return PA_ERR_ARG;
+  if (num_q_heads % pool.num_kv_heads) return PA_ERR_SHAPE;
+  const int group = num_q_heads / pool.num_kv_heads;
+  if (group > 16) return PA_ERR_UNSUPPORTED;
+  if (num_seqs == 0) return PA_OK;
+  if (max_q_len < 1 || (!cu_q_lens && (total_q != num_seqs || max_q_len != 1))) return PA_ERR_ARG;
+  const int64_t rows = static_cast<int64_t>(pool.num_blocks) * pool.num_kv_heads * 16;
+  if (max_q_len > PA_MASS_MAX_QUERIES || total_q >= (1 << 30) || rows >= (1LL << 31) ||
+      max_blocks_per_seq > (1 << 26))
+    return PA_ERR_UNSUPPORTED;
+  if (!q || !lse || !k_pool || !block_tables || !context_lens || !mass_out) return PA_ERR_ARG;
+  if (!aligned16(q) || !aligned16(k_pool)) return PA_ERR_ARG;
+  if (q_stride < static_cast<int64_t>(num_q_heads) * pool.head_dim || q_stride % 8)
+    return PA_ERR_ARG;
+  if (total_q == 0) return PA_ERR_ARG;
+  MassParams p = {};
+  p.err = device_error_word();
+  if (!p.err) return PA_ERR_CUDA;
+  p.lse = lse;
+  p.cu_q = cu_q_lens;
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.mass_in = mass_in;
+  p.mass_out = mass_out;
+  p.mass_stride = mass_stride;
+  p.total_q = total_q;
+  p.max_n = max_q_len;
+  p.max_blocks = max_blocks_per_seq;
+  p.num_blocks = pool.num_blocks;
+  p.hkv = pool.num_kv_heads;
+  p.hq = num_q_heads;
+  p.group = group;
+  p.tpt = 128 / group;
+  // (a decode step's tile: one query)
+  if (max_q_len < p.tpt) p.tpt = max_q_len;
+  p.num_seqs = num_seqs;
+  p.scale_log2 = scale * kLog2e;
+  const int64_t tiles = (static_cast<int64_t>(max_blocks_per_seq) * 16 + 127) / 128;
+  const int64_t most = tiles > num_sms() ? num_sms() : tiles * num_seqs * p.hkv;
+  if (pool.head_dim == 128)
+    return launch_mass<128>(p, q, q_stride, k_pool, pool, most, as_stream(stream));
+  return launch_mass<64>(p, q, q_stride, k_pool, pool, most, as_stream(stream));
+}
+
+}  // extern "C"

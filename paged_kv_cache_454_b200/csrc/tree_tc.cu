@@ -47,8 +47,8 @@
 #include <math_constants.h>
 
 #include "../../include/pa_tree.h"
+#include "draft_common.cuh"
 #include "internal.h"
-#include "tc_common.cuh"
 
 namespace pa {
 namespace {
@@ -124,20 +124,10 @@ struct __align__(64) TreeParams {
 // ---------------------------------------------------------------------------
 // Sequences, items and units
 // ---------------------------------------------------------------------------
-struct SeqRaw {
-  int q0, q1, L;
-};
-
 struct Seq {
   int q0, n, L;
   int tiles, passes;  // tiles 0: nothing to do
 };
-
-__device__ __forceinline__ int ld_i32(const int32_t* ptr) {
-  int x;
-  asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(x) : "l"(ptr));
-  return x;
-}
 
 __device__ __forceinline__ SeqRaw fetch_seq(const TreeParams& p, int s) {
   SeqRaw r;
@@ -183,11 +173,6 @@ struct Unit {
   bool pair;    // two row tiles
 };
 
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&b);
-}
-
 // 32 keys' visibility for one row, from key c + rel on: cached ones (rel < 0) are
 // seen, drafted ones by the row's mask (its first two words are at hand), ones
 // past the context are not.
@@ -201,24 +186,6 @@ __device__ __forceinline__ uint32_t mask_word(const uint32_t* row, uint2 head, i
 __device__ __forceinline__ uint32_t visible32(const uint32_t* row, uint2 head, int rel, int n) {
   const int j = rel >> 5;  // floor
   return __funnelshift_r(mask_word(row, head, j, n), mask_word(row, head, j + 1, n), rel & 31);
-}
-
-// One lane of a converged warp, always the same.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(r));
-  return r != 0;
-}
-
-// A wait of the unit ring: several times as long as the waits for data.
-__device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity, unsigned* err) {
-  for (int i = 0; i < 8; ++i)
-    if (mbar_wait(bar, parity, nullptr, err)) return true;
-  return false;
 }
 
 // OR of `pred` over the `count` threads of a named barrier.
@@ -320,20 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
     long long mine = 0;
     for (int s = s_lo; s < s_hi; ++s)
       mine += seq_places(decode_seq(p, fetch_seq(p, s), blockIdx.x == 0 ? p.err : nullptr), p.hkv);
-    long long scan = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, scan, o);
-      if (lane >= o) scan += v;
-    }
-    if (lane == 31) warp_sum[warp] = scan;
-    __syncthreads();
-    long long before = scan - mine;
-    total = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) before += warp_sum[w];
-      total += warp_sum[w];
-    }
+    const long long before = cta_scan<kThreads / 32>(mine, warp_sum, total);
     chunk = (total + gridDim.x - 1) / gridDim.x;
     if (chunk < kMinPlaces) chunk = kMinPlaces;
     const long long begin = chunk * blockIdx.x;
@@ -507,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
           mbar_wait(&kv_empty[slot], phase ^ 1, abort_flag, p.err);
-          if (!*abort_flag) {
+          if (!__any_sync(0xffffffffu, *abort_flag)) {
             if (lane == 0) {
               if (v == 0) kmask[kt % kMaskRing] = vm;
               mbar_arrive_expect_tx(&kv_full[slot], __popc(vm) * C::kPage);

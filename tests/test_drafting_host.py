@@ -93,6 +93,56 @@ def test_tree_refusals(lib):
         assert lib.pa_tree_workspace_size(*bad) == 0
 
 
+def test_mass_refusals(lib):
+    def call(q=FAKE, qs=512, lse=FAKE, cu=FAKE, total=6, max_n=5, kp=FAKE, desc=None, tables=FAKE,
+             blocks=4, lens=FAKE, seqs=2, hq=4, m_in=None, m_out=FAKE, stride=64):
+        return lib.pa_attention_mass(q, qs, lse, cu, total, max_n, kp, desc or pool(), tables,
+                                     blocks, lens, seqs, hq, 1.0, m_in, m_out, stride, None)
+    assert call(seqs=0) == _abi.PA_OK
+    for kw in (dict(q=None), dict(lse=None), dict(kp=None), dict(tables=None), dict(lens=None),
+               dict(m_out=None), dict(q=ODD), dict(kp=ODD), dict(qs=256), dict(qs=516),
+               dict(max_n=0), dict(seqs=-1), dict(total=-1), dict(blocks=0), dict(hq=0),
+               dict(stride=-1), dict(cu=None), dict(cu=None, total=2)):
+        refuse(call, _abi.PA_ERR_ARG, **kw)
+    refuse(call, _abi.PA_ERR_SHAPE, hq=3)
+    for kw in (dict(hq=34, qs=34 * 128), dict(desc=pool(d=96)), dict(max_n=(1 << 20) + 1),
+               dict(desc=pool(nb=1 << 27))):
+        refuse(call, _abi.PA_ERR_UNSUPPORTED, **kw)
+
+
+def test_evict_refusals(lib):
+    def call(mass=FAKE, stride=64, kp=FAKE, vp=FAKE, desc=None, tables=FAKE, blocks=4, lens=FAKE,
+             budgets=FAKE, sink=1, recent=1, new=None, new_blocks=0, kept=FAKE, kept_stride=8,
+             new_lens=ctypes.c_void_p(0x20000), m_out=ctypes.c_void_p(0x30000), out_stride=8,
+             seqs=2):
+        return lib.pa_evict(mass, stride, kp, vp, desc or pool(), tables, blocks, lens, budgets,
+                            sink, recent, new, new_blocks, kept, kept_stride, new_lens, m_out,
+                            out_stride, seqs, None)
+    assert call(seqs=0) == _abi.PA_OK
+    for kw in (dict(mass=None), dict(kp=None), dict(vp=ODD), dict(tables=None), dict(lens=None),
+               dict(budgets=None), dict(kept=None), dict(new_lens=None), dict(m_out=None),
+               dict(new_lens=FAKE), dict(sink=-1), dict(recent=-1), dict(seqs=-1), dict(blocks=0),
+               dict(stride=-1), dict(kept_stride=-1), dict(new=ctypes.c_void_p(0x40000)),
+               dict(new=FAKE, new_blocks=4), dict(m_out=FAKE)):
+        refuse(call, _abi.PA_ERR_ARG, **kw)
+    refuse(call, _abi.PA_ERR_UNSUPPORTED, desc=pool(bs=8))
+    refuse(call, _abi.PA_ERR_UNSUPPORTED, blocks=(1 << 26) + 1)
+
+
+def test_compact_refusals(lib):
+    def call(kp=FAKE, vp=FAKE, desc=None, tables=FAKE, blocks=4, new=None, new_blocks=0, base=None,
+             kept=FAKE, heads=2, stride=8, counts=FAKE, seqs=2):
+        return lib.pa_compact_tokens(kp, vp, desc or pool(), tables, blocks, new, new_blocks, base,
+                                     kept, heads, stride, counts, seqs, None)
+    assert call(seqs=0) == _abi.PA_OK and call(stride=0) == _abi.PA_OK
+    for kw in (dict(kp=None), dict(vp=None), dict(kp=ODD), dict(tables=None), dict(kept=None),
+               dict(counts=None), dict(blocks=0), dict(seqs=-1), dict(stride=-1),
+               dict(new=ctypes.c_void_p(0x40000)), dict(new=FAKE, new_blocks=4)):
+        refuse(call, _abi.PA_ERR_ARG, **kw)
+    refuse(call, _abi.PA_ERR_SHAPE, heads=3)
+    refuse(call, _abi.PA_ERR_UNSUPPORTED, desc=pool(d=32))
+
+
 def test_frequencies():
     f, factor = pa.pa_rope_frequencies(8)
     assert factor == 1.0 and np.allclose(f, [1, 0.1, 0.01, 0.001], rtol=1e-15)
@@ -219,6 +269,8 @@ def test_oracle_evict_by_hand():
     assert choose(8, 2, 5, 5) == [0, 1]
     assert choose(8, 8, 0, 0) == list(range(8)) and choose(3, 100, 1, 1) == [0, 1, 2]
     assert choose(8, 7, 0, 0) == [0, 1, 2, 3, 5, 6, 7]   # NaN goes first
+    low = np.array([np.nan, -np.inf, -1.0])
+    assert drafting.evict_choice(low, 3, 2, 0, 0).tolist() == [1, 2]
     assert choose(8, 0, 2, 2) == [] and choose(0, 5, 1, 1) == []
 
 
