@@ -5,11 +5,17 @@
 // unsigned keys of the same order and stay in registers (up to 32 per thread);
 // the key of the last token that fits is found bit by bit from the top -- a
 // candidate threshold, a count of the keys at or above it, one barrier -- until
-// a count hits the wanted number exactly or the bits run out.  Then every token
-// above the threshold is kept, and of those at it the lowest indices.  A warp
-// owns a run of tokens, so counts of ballots give each kept token its place in
-// order without sorting.  Longer rows (evict_select_long_kernel) do the same
-// over the row in memory, eight bits at a time with a histogram per warp.
+// a count hits the wanted number exactly or the bits run out.  As soon as no more
+// keys share the threshold's bits than there are threads (after a dozen bits of a
+// spread row), only those are looked at, one each.  Then every token above the
+// threshold is kept, and of those at it the lowest indices.  A warp owns a run of
+// tokens, so counts of ballots give each kept token its place in order without
+// sorting.  A small CTA takes a row of up to 8192 tokens, so that several rows
+// share an SM.  Longer rows, and any where there are few, are shared by a cluster
+// of eight CTAs (evict_select_cluster_kernel): the same steps, two bits at a time,
+// the counts of all warps exchanged through distributed shared memory.  Rows past
+// 131072 tokens (evict_select_long_kernel) are read again for every eight bits,
+// with a histogram per warp.
 //
 // Move (compact): rows of 16-byte chunks.  Into fresh blocks all rows move at
 // once; in place a CTA takes one slice of the columns of one (sequence, head),
@@ -19,6 +25,8 @@
 //
 // Bound: HBM for the move (each kept row read and written once); the choice is
 // bound by its steps' latency.
+#include <cooperative_groups.h>
+
 #include <algorithm>
 
 #include "../../include/pa_evict.h"
@@ -31,9 +39,8 @@ namespace {
 // ---------------------------------------------------------------------------
 // Choice
 // ---------------------------------------------------------------------------
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 1024;  // of the long rows' kernel
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelMost = 32;  // tokens per thread in registers: up to 32768 a row
 
 struct SelectParams {
   const float* mass;
@@ -86,20 +93,24 @@ __device__ __forceinline__ float weight_of(uint32_t key) {
   return __uint_as_float((key & 0x80000000u) ? key & 0x7fffffffu : ~key);
 }
 
-// Sum over the CTA of one number per thread; `slots` alternates between two
-// arrays so that one barrier is enough.
+// Sum over a CTA of `kWarps` warps of one number per thread; `slots` alternates
+// between two arrays so that one barrier is enough.
+template <int kWarps>
 __device__ __forceinline__ int cta_sum(int x, int* slots, int warp, int lane) {
   const int w = __reduce_add_sync(0xffffffffu, x);
   if (lane == 0) slots[warp] = w;
   __syncthreads();
-  return __reduce_add_sync(0xffffffffu, slots[lane]);
+  return __reduce_add_sync(0xffffffffu, lane < kWarps ? slots[lane] : 0);
 }
 
-// Where this warp's kept tokens and ties begin: sums over the warps before it.
-__device__ __forceinline__ int2 warps_before(int2 x, int2* slots, int warp, int lane) {
+// Where this warp's kept tokens and ties begin: sums over the warps before it; and
+// the sums over all.
+template <int kWarps>
+__device__ __forceinline__ int2 warps_before(int2 x, int2* slots, int warp, int lane, int2& all) {
   if (lane == 0) slots[warp] = x;
   __syncthreads();
-  const int2 v = slots[lane];
+  const int2 v = lane < kWarps ? slots[lane] : make_int2(0, 0);
+  all = make_int2(__reduce_add_sync(0xffffffffu, v.x), __reduce_add_sync(0xffffffffu, v.y));
   return make_int2(__reduce_add_sync(0xffffffffu, lane < warp ? v.x : 0),
                    __reduce_add_sync(0xffffffffu, lane < warp ? v.y : 0));
 }
@@ -107,26 +118,32 @@ __device__ __forceinline__ int2 warps_before(int2 x, int2* slots, int warp, int 
 // The kept tokens of a row, in order, from per-thread flags of one token each
 // (`sure`: forced or above the threshold; `at`: at it), for tokens that follow
 // one another along the lanes.  place and tie are the warp's running counts: kept
-// tokens, and ties, before these.
-__device__ __forceinline__ int place_of(bool sure, bool at, int ties, int lane, int& place,
-                                        int& tie) {
+// tokens, and ties, before these.  `no_ties`: no token is at it.
+__device__ __forceinline__ int place_of(bool sure, bool at, bool no_ties, int ties, int lane,
+                                        int& place, int& tie) {
   const uint32_t below = (1u << lane) - 1u;
-  const uint32_t ats = __ballot_sync(0xffffffffu, at);
-  const bool keep = sure || (at && tie + __popc(ats & below) < ties);
+  bool keep = sure;
+  if (!no_ties) {
+    const uint32_t ats = __ballot_sync(0xffffffffu, at);
+    keep = sure || (at && tie + __popc(ats & below) < ties);
+    tie += __popc(ats);
+  }
   const uint32_t keeps = __ballot_sync(0xffffffffu, keep);
   const int i = place + __popc(keeps & below);
   place += __popc(keeps);
-  tie += __popc(ats);
   return keep ? i : -1;
 }
 
 // ITEMS: tokens per lane at most.  Lane l's item k of warp w is token
-// (w * items + k) * 32 + l, items = ceil(len / 1024).
-template <int ITEMS>
-__global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(
-    const __grid_constant__ SelectParams p) {
-  __shared__ int sums[2][kSelWarps];
-  __shared__ int2 bases[kSelWarps];
+// (w * items + k) * 32 + l, items = ceil(len / THREADS).
+template <int THREADS, int ITEMS>
+__global__ void __launch_bounds__(THREADS, 768 / THREADS)
+    evict_select_kernel(const __grid_constant__ SelectParams p) {
+  constexpr int kWarps = THREADS / 32;
+  __shared__ int sums[2][kWarps];
+  __shared__ int2 bases[kWarps];
+  __shared__ uint32_t close[THREADS];  // the keys that share the threshold's bits
+  __shared__ int n_close;
   // the move may be set up now (it waits for this grid's end)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int row = blockIdx.x;
@@ -136,56 +153,242 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(
   if (row % p.hkv == 0 && tid == 0) p.new_lens[s] = c.keep;
   if (c.keep == 0) return;
   const float* mass = p.mass + row * p.mass_stride;
-  const int items = (c.len + kSelThreads - 1) / kSelThreads;
+  const int items = (c.len + THREADS - 1) / THREADS;
   const int first = warp * items * 32 + lane;
   const int lo = c.sink, hi = c.len - c.recent;  // the tokens with a choice
+  int32_t* kept = p.kept + static_cast<int64_t>(row) * p.kept_stride;
+  float* out = p.mass_out + row * p.mass_out_stride;
+  if (tid == 0) n_close = 0;
+  // (every load is made, of the last token where there is none: then they all are
+  // on their way at once)
   uint32_t key[ITEMS];
-  uint32_t open = 0, forced = 0;  // bit k: item k has a choice, is kept anyway
+#pragma unroll
+  for (int k = 0; k < ITEMS; ++k)
+    key[k] = __float_as_uint(mass[min(first + 32 * min(k, items - 1), c.len - 1)]);
+#pragma unroll
+  for (int k = 0; k < ITEMS; ++k) key[k] = key_of(__uint_as_float(key[k]));
+  __syncthreads();  // all weights are read: in place, theirs may be overwritten
+  // Tokens kept anyway have their places already; `open`: the others, whose key
+  // counts (a key of 0 reaches no threshold).
+  uint32_t open = 0;
 #pragma unroll
   for (int k = 0; k < ITEMS; ++k) {
     const int t = first + 32 * k;
-    const bool live = k < items && t < c.len;
-    key[k] = live ? key_of(mass[t]) : 0u;
-    if (live && t >= lo && t < hi && c.need > 0) open |= 1u << k;
-    if (live && (t < lo || t >= hi)) forced |= 1u << k;
+    if (k < items && t >= lo && t < hi) {
+      open |= 1u << k;
+    } else {
+      if (k < items && t < c.len) {
+        const int i = t < lo ? t : c.keep - (c.len - t);
+        kept[i] = t;
+        out[i] = weight_of(key[k]);
+      }
+      key[k] = 0;
+    }
   }
+  if (c.need == 0) return;
   // The largest threshold that at least `need` keys reach.
   uint32_t bar = 0;
   int above = hi - lo;  // keys at or above the threshold (0: all with a choice)
-  if (c.need > 0 && c.need < hi - lo) {
-    for (int b = 31; b >= 0 && above != c.need; --b) {
+  int over = 0;         // keys above all that share its bits so far
+  if (c.need < hi - lo) {
+    int b = 31;
+    for (; b >= 0 && above != c.need && above - over > THREADS; --b) {
       const uint32_t cand = bar | (1u << b);
-      uint32_t m = 0;
+      int mine = 0;
 #pragma unroll
-      for (int k = 0; k < ITEMS; ++k) m |= key[k] >= cand ? 1u << k : 0u;
-      const int n = cta_sum(__popc(m & open), sums[b & 1], warp, lane);
+      for (int k = 0; k < ITEMS; ++k) mine += key[k] >= cand;
+      const int n = cta_sum<kWarps>(mine, sums[b & 1], warp, lane);
       if (n >= c.need) {
         bar = cand;
         above = n;
+      } else {
+        over = n;
+      }
+    }
+    if (b >= 0 && above != c.need) {
+      // the keys in [bar, bar + 2^(b + 1)), in any order: a warp's share of the
+      // list at a time
+      const uint32_t span = b == 31 ? 0xffffffffu : (2u << b) - 1u;
+      uint32_t in = 0;
+#pragma unroll
+      for (int k = 0; k < ITEMS; ++k)
+        if (key[k] - bar <= span) in |= open & (1u << k);
+      const int n_in = __popc(in);
+      int upto = n_in;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+      }
+      int base = 0;
+      if (lane == 31) base = atomicAdd(&n_close, upto);
+      base = __shfl_sync(0xffffffffu, base, 31) + upto - n_in;
+#pragma unroll
+      for (int k = 0; k < ITEMS; ++k)
+        if ((in >> k) & 1u) close[base++] = key[k];
+      __syncthreads();
+      const uint32_t mine = tid < n_close ? close[tid] : 0u;
+      for (; b >= 0 && above != c.need; --b) {
+        const uint32_t cand = bar | (1u << b);
+        const int n = over + cta_sum<kWarps>(mine >= cand, sums[b & 1], warp, lane);
+        if (n >= c.need) {
+          bar = cand;
+          above = n;
+        }
       }
     }
   }
-  // Above the threshold: kept; at it: the first ones in order, as many as fit.
-  uint32_t sure = forced, at = 0;
+  // Above the threshold: kept; at it: the first ones in order, as many as fit (all
+  // of them where the count was hit exactly: then they count as above).
+  const bool exact = above == c.need;
+  const uint32_t least = exact ? bar : bar + 1;  // (bar + 1 is 0 for no key there is)
+  uint32_t sure = 0, at = 0;
 #pragma unroll
   for (int k = 0; k < ITEMS; ++k) {
-    if (key[k] > bar) sure |= open & (1u << k);
-    if (key[k] == bar) at |= open & (1u << k);
+    if (key[k] >= least) sure |= 1u << k;
+    if (key[k] == bar) at |= 1u << k;
   }
+  sure &= open;
+  at = exact ? 0u : at & open;
   const int2 mine = make_int2(__reduce_add_sync(0xffffffffu, __popc(sure)),
                               __reduce_add_sync(0xffffffffu, __popc(at)));
-  const int2 before = warps_before(mine, bases, warp, lane);
-  const int ties = c.keep - cta_sum(lane == 0 ? mine.x : 0, sums[0], warp, lane);
-  int place = before.x + min(before.y, ties), tie = before.y;
-  int32_t* kept = p.kept + static_cast<int64_t>(row) * p.kept_stride;
-  float* out = p.mass_out + row * p.mass_out_stride;
+  int2 all;
+  const int2 before = warps_before<kWarps>(mine, bases, warp, lane, all);
+  const int ties = c.need - all.x;
+  int place = c.sink + before.x + min(before.y, ties), tie = before.y;
 #pragma unroll
   for (int k = 0; k < ITEMS; ++k) {
     if (k < items) {
-      const int i = place_of((sure >> k) & 1u, (at >> k) & 1u, ties, lane, place, tie);
+      const int i = place_of((sure >> k) & 1u, (at >> k) & 1u, exact, ties, lane, place, tie);
       if (i >= 0) {
         kept[i] = first + 32 * k;
-        out[i] = weight_of(key[k]);  // (all weights were read before the last barrier)
+        out[i] = weight_of(key[k]);
+      }
+    }
+  }
+}
+
+// A row shared by a cluster of eight CTAs: lane l's item k of the cluster's warp w
+// is token (w * items + k) * 32 + l.
+constexpr int kSelCluster = 8;
+
+template <int THREADS, int ITEMS>
+__global__ void __cluster_dims__(kSelCluster, 1, 1) __launch_bounds__(THREADS, 1)
+    evict_select_cluster_kernel(const __grid_constant__ SelectParams p) {
+  namespace cg = cooperative_groups;
+  constexpr int kWarps = THREADS / 32 * kSelCluster;  // of the cluster
+  __shared__ int4 counts[2][kWarps];  // every warp's, in every CTA; in turn
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = static_cast<int>(cluster.block_rank());
+  const int row = blockIdx.x / kSelCluster;
+  const int s = row / p.hkv;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = rank * (THREADS / 32) + (tid >> 5);
+  const bool lead = row % p.hkv == 0 && rank == 0 && tid == 0;
+  const Choice c = choice_of(p, s, lead);
+  if (lead) p.new_lens[s] = c.keep;
+  if (c.keep == 0) return;  // the whole cluster
+  const float* mass = p.mass + row * p.mass_stride;
+  const int items = (c.len + 32 * kWarps - 1) / (32 * kWarps);
+  const int first = warp * items * 32 + lane;
+  const int lo = c.sink, hi = c.len - c.recent;
+  int32_t* kept = p.kept + static_cast<int64_t>(row) * p.kept_stride;
+  float* out = p.mass_out + row * p.mass_out_stride;
+  uint32_t key[ITEMS];
+#pragma unroll
+  for (int k = 0; k < ITEMS; ++k)
+    key[k] = __float_as_uint(mass[min(first + 32 * min(k, items - 1), c.len - 1)]);
+#pragma unroll
+  for (int k = 0; k < ITEMS; ++k) key[k] = key_of(__uint_as_float(key[k]));
+  cluster.sync();  // all weights are read (and all CTAs have started)
+  uint32_t open = 0;
+#pragma unroll
+  for (int k = 0; k < ITEMS; ++k) {
+    const int t = first + 32 * k;
+    if (k < items && t >= lo && t < hi) {
+      open |= 1u << k;
+    } else {
+      if (k < items && t < c.len) {
+        const int i = t < lo ? t : c.keep - (c.len - t);
+        kept[i] = t;
+        out[i] = weight_of(key[k]);
+      }
+      key[k] = 0;
+    }
+  }
+  if (c.need == 0) return;
+  // Every warp's numbers in every CTA: lane j of a warp writes CTA j's copy.
+  int turn = 0;
+  auto exchange = [&](int4 mine) -> int4* {
+    int4* slots = counts[turn++ & 1];
+    if (lane < kSelCluster) *cluster.map_shared_rank(&slots[warp], lane) = mine;
+    cluster.sync();
+    return slots;
+  };
+  uint32_t bar = 0;
+  int above = hi - lo;
+  if (c.need < hi - lo) {
+    for (int b = 30; b >= 0 && above != c.need; b -= 2) {
+      const uint32_t cand = bar | (1u << b);
+      int n1 = 0, n2 = 0, n3 = 0;
+#pragma unroll
+      for (int k = 0; k < ITEMS; ++k) {
+        n1 += key[k] >= cand;
+        n2 += key[k] >= cand + (1u << b);
+        n3 += key[k] >= cand + (2u << b);
+      }
+      n1 = __reduce_add_sync(0xffffffffu, n1);
+      n2 = __reduce_add_sync(0xffffffffu, n2);
+      n3 = __reduce_add_sync(0xffffffffu, n3);
+      const int4* slots = exchange(make_int4(n1, n2, n3, 0));
+      n1 = n2 = n3 = 0;
+      for (int w = lane; w < kWarps; w += 32) {
+        n1 += slots[w].x;
+        n2 += slots[w].y;
+        n3 += slots[w].z;
+      }
+      n1 = __reduce_add_sync(0xffffffffu, n1);
+      n2 = __reduce_add_sync(0xffffffffu, n2);
+      n3 = __reduce_add_sync(0xffffffffu, n3);
+      const int steps = n3 >= c.need ? 3 : n2 >= c.need ? 2 : n1 >= c.need ? 1 : 0;
+      bar += static_cast<uint32_t>(steps) << b;
+      above = steps == 3 ? n3 : steps == 2 ? n2 : steps == 1 ? n1 : above;
+    }
+  }
+  const bool exact = above == c.need;
+  const uint32_t least = exact ? bar : bar + 1;
+  uint32_t sure = 0, at = 0;
+#pragma unroll
+  for (int k = 0; k < ITEMS; ++k) {
+    if (key[k] >= least) sure |= 1u << k;
+    if (key[k] == bar) at |= 1u << k;
+  }
+  sure &= open;
+  at = exact ? 0u : at & open;
+  const int4* slots = exchange(make_int4(__reduce_add_sync(0xffffffffu, __popc(sure)),
+                                         __reduce_add_sync(0xffffffffu, __popc(at)), 0, 0));
+  int before_sure = 0, before_at = 0, all_sure = 0;
+  for (int w = lane; w < kWarps; w += 32) {
+    const int4 v = slots[w];
+    all_sure += v.x;
+    if (w < warp) {
+      before_sure += v.x;
+      before_at += v.y;
+    }
+  }
+  all_sure = __reduce_add_sync(0xffffffffu, all_sure);
+  before_sure = __reduce_add_sync(0xffffffffu, before_sure);
+  before_at = __reduce_add_sync(0xffffffffu, before_at);
+  const int ties = c.need - all_sure;
+  int place = c.sink + before_sure + min(before_at, ties), tie = before_at;
+#pragma unroll
+  for (int k = 0; k < ITEMS; ++k) {
+    if (k < items) {
+      const int i = place_of((sure >> k) & 1u, (at >> k) & 1u, exact, ties, lane, place, tie);
+      if (i >= 0) {
+        kept[i] = first + 32 * k;
+        out[i] = weight_of(key[k]);
       }
     }
   }
@@ -257,7 +460,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_long_kernel(
   int n_sure = 0;
   for (int t = lo + tid; t < hi; t += kSelThreads) n_sure += c.need > 0 && key_of(mass[t]) > bar;
   __syncthreads();
-  n_sure = cta_sum(n_sure, hist[0], warp, lane);
+  n_sure = cta_sum<kSelWarps>(n_sure, hist[0], warp, lane);
   const int ties = c.need - n_sure;
   int32_t* kept = p.kept + static_cast<int64_t>(row) * p.kept_stride;
   float* out = p.mass_out + row * p.mass_out_stride;
@@ -270,18 +473,17 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_long_kernel(
     const bool at = open && k == bar;
     const int2 mine = make_int2(__popc(__ballot_sync(0xffffffffu, sure)),
                                 __popc(__ballot_sync(0xffffffffu, at)));
-    int2* slots = bases[turn & 1];
-    const int2 before = warps_before(mine, slots, warp, lane);
+    int2 all;
+    const int2 before = warps_before<kSelWarps>(mine, bases[turn & 1], warp, lane, all);
     int tie = ties_done + before.y;
     int place = done + before.x + min(tie, ties);
-    const int i = place_of(sure, at, ties, lane, place, tie);
+    const int i = place_of(sure, at, false, ties, lane, place, tie);
     if (i >= 0) {  // (i <= t: this turn's weights are read, later ones lie beyond)
       kept[i] = t;
       out[i] = weight_of(k);
     }
-    const int2 v = slots[lane];
-    done += __reduce_add_sync(0xffffffffu, v.x);
-    ties_done += __reduce_add_sync(0xffffffffu, v.y);
+    done += all.x;
+    ties_done += all.y;
   }
 }
 
@@ -466,9 +668,15 @@ int run_move(MoveParams& p, int head_dim, bool dependent, cudaStream_t stream) {
                                 dependent, stream);
 }
 
-template <int ITEMS>
+template <int THREADS, int ITEMS>
 int launch_select(const SelectParams& p, int rows, cudaStream_t stream) {
-  evict_select_kernel<ITEMS><<<rows, kSelThreads, 0, stream>>>(p);
+  evict_select_kernel<THREADS, ITEMS><<<rows, THREADS, 0, stream>>>(p);
+  return launch_status();
+}
+
+template <int THREADS, int ITEMS>
+int launch_select_cluster(const SelectParams& p, int rows, cudaStream_t stream) {
+  evict_select_cluster_kernel<THREADS, ITEMS><<<rows * kSelCluster, THREADS, 0, stream>>>(p);
   return launch_status();
 }
 
@@ -501,7 +709,7 @@ int pa_evict(const float* mass, int64_t mass_stride, void* k_pool, void* v_pool,
   if (new_tables && (new_max_blocks <= 0 || new_tables == block_tables)) return PA_ERR_ARG;
   if (mass_out == mass && mass_out_stride != mass_stride) return PA_ERR_ARG;
   const int64_t rows = static_cast<int64_t>(num_seqs) * pool.num_kv_heads;
-  if (rows > 0x7fffffff || table_tokens(max_blocks_per_seq) > (1 << 30)) return PA_ERR_UNSUPPORTED;
+  if (rows > 0x7fffffff / kSelCluster || table_tokens(max_blocks_per_seq) > (1 << 30)) return PA_ERR_UNSUPPORTED;
   SelectParams p = {};
   p.err = device_error_word();
   if (!p.err) return PA_ERR_CUDA;
@@ -518,19 +726,21 @@ int pa_evict(const float* mass, int64_t mass_stride, void* k_pool, void* v_pool,
   p.mass_out_stride = mass_out_stride;
   p.hkv = pool.num_kv_heads;
   p.most_len = static_cast<int>(table_tokens(max_blocks_per_seq));
-  // the longest row there can be decides how many tokens a thread holds
+  // the longest row there can be, and whether one CTA per row leaves most of the
+  // device idle, decide the kernel
   const int64_t longest = std::min<int64_t>(p.most_len, mass_stride);
   const int r = static_cast<int>(rows);
-  if (longest <= 4 * kSelThreads)
-    st = launch_select<4>(p, r, as_stream(stream));
-  else if (longest <= 8 * kSelThreads)
-    st = launch_select<8>(p, r, as_stream(stream));
-  else if (longest <= 16 * kSelThreads)
-    st = launch_select<16>(p, r, as_stream(stream));
-  else if (longest <= kSelMost * kSelThreads)
-    st = launch_select<kSelMost>(p, r, as_stream(stream));
+  cudaStream_t cs = as_stream(stream);
+  if (longest <= 8192 && rows * kSelCluster > 2 * num_sms())
+    st = longest <= 2048 ? launch_select<256, 8>(p, r, cs) : launch_select<256, 32>(p, r, cs);
+  else if (longest <= 8192)
+    st = launch_select_cluster<256, 4>(p, r, cs);
+  else if (longest <= 32768)
+    st = launch_select_cluster<256, 16>(p, r, cs);
+  else if (longest <= 131072)
+    st = launch_select_cluster<1024, 16>(p, r, cs);
   else {
-    evict_select_long_kernel<<<r, kSelThreads, 0, as_stream(stream)>>>(p);
+    evict_select_long_kernel<<<r, kSelThreads, 0, cs>>>(p);
     st = launch_status();
   }
   if (st != PA_OK || kept_stride == 0) return st;

@@ -102,8 +102,11 @@ CASES = [  # lens, hkv, d, budgets, sink, recent
     ([4097, 2000], 1, 64, [2049, 1], 3, 3),          # eight tokens a thread
     ([9000], 2, 128, [1531], 16, 256),               # sixteen
     ([20011, 31], 1, 128, [4096, 8], 4, 64),         # thirty-two
-    ([33000, 500], 1, 64, [3001, 500], 5, 77),       # the long rows' kernel
+    ([33000, 500], 1, 64, [3001, 500], 5, 77),
     ([70001], 2, 64, [65000], 0, 1),
+    ([100] * 20, 2, 64, [50] * 20, 2, 5),            # a CTA per row: up to 2048 tokens
+    ([5000, 100, 8192] + [64] * 37, 1, 64, [700] * 40, 2, 5),   # and up to 8192
+    ([140000], 1, 64, [30000], 4, 1000),             # past what a cluster holds
 ]
 
 
@@ -113,7 +116,7 @@ def test_evict(lens, hkv, d, budgets, sink, recent, new):
     Batch(sum(lens) + hkv, lens, hkv, d).check(budgets, sink, recent, new)
 
 
-@pytest.mark.parametrize("length", [700, 5000, 40000])
+@pytest.mark.parametrize("length", [700, 5000, 40000, 132000])
 def test_evict_ties_go_to_the_lowest_index(length):
     b = Batch(3, [length, length // 2], 2, 64, ties=True)
     b.check([length // 3, length // 3], 2, 9, new=True)
@@ -122,18 +125,18 @@ def test_evict_ties_go_to_the_lowest_index(length):
     b.check([length // 3, length // 4], 0, 5, new=False)
 
 
-@pytest.mark.parametrize("length", [500, 6000, 36000])
+@pytest.mark.parametrize("length", [500, 6000, 6001, 36000, 133000])
 def test_evict_unusual_weights(length):
     # NaN is the least, infinities and denormals keep their order
-    b = Batch(5, [length], 2, 64)
+    b = Batch(5, [length] + [1] * 40, 2, 64) if length == 6001 else Batch(5, [length], 2, 64)
     m = b.mass[0, 0]
     m[:] = b.rng.choice(np.array([np.nan, np.inf, -np.inf, 1e-45, 3e-45, -1e-45, 0.0, -2.5, 7.0],
                                  np.float32), length)
     order = np.argsort(b.rng.random(length))
     b.mass[0, 1] = (order * np.float32(1e-45)).astype(np.float32)  # denormals only
     for budget in (length // 5, length // 2, length - 3):
-        b.check([budget], 1, 1, new=True)
-    b.check([length // 2], 0, 0, new=False, in_place_mass=True)
+        b.check([budget] * len(b.lens), 1, 1, new=True)
+    b.check([length // 2] * len(b.lens), 0, 0, new=False, in_place_mass=True)
 
 
 def test_evict_bounds_and_strides():
