@@ -4,30 +4,32 @@
 // The G = Hq/Hkv query heads of a sequence's n drafted tokens form rows (token,
 // head), token-major; floor(128/G) tokens make one 128-row tile, and an item is
 // (sequence, KV head, pass of up to two row tiles) over the sequence's key tiles
-// of 128.  Per row tile and key tile
-//     S [128 x 128] = Q . K^T            (D/16 MMAs)
-//     O [128 x D]  += P . V              (8 MMAs of P_hi, 8 of P_lo)
+// of 128, half a tile (64 keys) per step:
+//     S [128 x 64] = Q . K^T             (D/16 MMAs)
+//     O [128 x D] += P . V               (4 MMAs of P_hi, 4 of P_lo)
 // with fp32 accumulators in tensor memory; P = P_hi + P_lo, the weight with its
 // mantissa cut to bf16 and the same cut of the rest, replaces its scores in
-// tensor memory (per 32 keys: 16 columns of P_hi, 16 of P_lo) and is read there
-// by the second product.
+// tensor memory (per 16 keys: 8 columns of P_hi, 8 of P_lo) and is read there by
+// the second product.
 //
-// Two streams of (row tile, key tile) steps run side by side, each with its own
-// scores, accumulator and two softmax warpgroups (a thread owns 64 keys of a
-// row), so the tensor cores work for one while the other's softmax runs:
+// Two streams of (row tile, key tile) run side by side, each with its own scores,
+// accumulator and softmax warpgroup (a thread owns a row):
 //   pair mode    (two row tiles): stream h takes row tile h, both take every key
 //                tile; K and V are read once for up to 256 rows.
 //   split mode   (one row tile): both take the same rows, stream h the key tiles
 //                h, h+2, ...; their results meet by log-sum-exp at the end.
-// The maximum that a row's weights are formed with is the same in both halves of
-// the row and stays until a tile's maximum exceeds it by 2^16: the two warps that
-// share 32 rows vote once per step (an OR-reducing barrier of 64 threads); only
-// then they exchange maxima and rescale their rows of the accumulator.
+// A stream has two buffers of scores, one per half of a tile: while the softmax
+// works on one half, the other's weights are multiplied and the half after that
+// is scored (with one buffer of a whole tile, scores, softmax and product follow
+// each other and the tensor cores idle half the time: 533 against 404 us on 48
+// sequences).  A thread takes its 64 scores into registers once and puts the
+// weights back once: tensor memory answers between products, so every round trip
+// to it waits.
 //
-// Work split: all items' key tiles, in order, are one line, with kItemCost more
-// places in front of every item for what it costs besides its tiles, and every
-// CTA takes an equal stretch of it (each finds its start from the lengths by a
-// scan of its own: no plan kernel, no queue).  An item inside one CTA's stretch
+// Work split: all items' key tiles, in order, are one line, on which a tile has
+// places for its time and an item more in front of them for what it costs besides,
+// and every CTA takes an equal stretch of it (each finds its start from the lengths
+// by a scan of its own: no plan kernel, no queue).  An item inside one CTA's stretch
 // is finished there; one that crosses a border leaves normalised fp32 partial
 // rows and base-2 log-sum-exps in the workspace -- at most two items per CTA --
 // and a second kernel, a programmatic dependent, merges them.
@@ -40,7 +42,7 @@
 // both left the tensor cores idle for a third of the time: what it does between
 // two products is short, but every instruction of it waits among those of the
 // softmax warps), warp 3 walks the stretch, publishes its units in a ring and
-// copies their q, warps 4-19 are the softmax warpgroups (stream, key half).
+// copies their q, warps 4-11 are the two streams' softmax warpgroups.
 // Every wait on an mbarrier is bounded.  The named barriers join softmax warps
 // that go through the same units and steps whatever happens: after a time-out
 // the data waits return at once and the unit ring still runs to its end.
@@ -55,23 +57,25 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 640;
+constexpr int kThreads = 384;
 constexpr int kMaxCtas = 160;      // partial results are sized for this many
-constexpr int kMinPlaces = 2;      // places of a stretch at least
-constexpr int kItemCost = 2;       // places in front of an item
+// Places on the line, from a fit of the CTAs' cycles to what they had (a tile 3100
+// to 3500 in split mode, 3700 in pair mode; an item 4200 and 12700 besides).
+constexpr int kSplitTile = 5, kPairTile = 6;
+constexpr int kSplitItem = 7, kPairItem = 22;  // in front of an item's tiles
+constexpr int kMinPlaces = 10;                 // of a stretch
 constexpr int kRegion = 128 * 128; // 128 rows x 128 bytes
 constexpr int kQSlots = 2;
 constexpr int kUnits = 4;          // ring of units
-constexpr int kUnitReaders = 3 + 16;  // K/V, MMA and softmax warps
+constexpr int kUnitReaders = 3 + 8;  // K/V, MMA and softmax warps
 constexpr int kMaskRing = 16;
 constexpr float kRaiseLog2 = 16.f; // raise the maximum in use only past 2^16
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kOCol = 256;    // S_h at column 128 h, O_h at 256 + 128 h
+constexpr uint32_t kOCol = 256;    // S of stream h, half b at column 128 h + 64 b; O_h at 256 + 128 h
 
 // Named barriers.
 constexpr int kBarBoth = 1;    // all softmax warps
 constexpr int kBarStream = 2;  // + h: the warps of one stream
-constexpr int kBarPair = 4;    // + 4 h + warp: the two warps of 32 rows
 
 template <int D>
 struct Cfg {
@@ -84,12 +88,12 @@ struct Cfg {
   static constexpr int kOffUnit = kOffKV + kSlots * kTileBytes;  // [kUnits] x 48 bytes
   static constexpr int kOffX = kOffUnit + kUnits * 48;  // [4][128] floats: exchanges of a row
   static constexpr int kOffBar = kOffX + 4 * 128 * 4;
-  static constexpr int kNumBars = 2 * kQSlots + 2 * kSlots + 2 * kUnits + 6 + 3;
+  static constexpr int kNumBars = 2 * kQSlots + 2 * kSlots + 2 * kUnits + 12 + 3;
   // tensor-memory slot, abort flag, plan {sequence, place in it (8 bytes)}
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kOffMask = kOffMisc + 24;
-  static constexpr int kOffPoison = kOffMask + 4 * kMaskRing;  // [3 sets][2][2 halves][4 words]
-  static constexpr int kSmem = kOffPoison + 3 * 2 * 2 * 16;
+  static constexpr int kOffPoison = kOffMask + 4 * kMaskRing;  // [3 sets][2][4 words]
+  static constexpr int kSmem = kOffPoison + 3 * 2 * 16;
   static_assert(kSmem <= 232448, "shared memory per CTA");
 };
 
@@ -152,10 +156,25 @@ __device__ __forceinline__ Seq decode_seq(const TreeParams& p, const SeqRaw& r, 
   return q;
 }
 
-// Places of an item on the line, and of a sequence.
-__device__ __forceinline__ int item_places(const Seq& q) { return q.tiles + kItemCost; }
-__device__ __forceinline__ long long seq_places(const Seq& q, int hkv) {
-  return q.tiles ? static_cast<long long>(item_places(q)) * q.passes * hkv : 0;
+// Places on the line of one item of pass rp, as what lies in front of its tiles and
+// each of them; and of a head (all passes but the last have two row tiles).
+struct Places {
+  int front, each;
+};
+__device__ __forceinline__ Places places_of(const Seq& q, int rp, int tpt) {
+  return q.n - rp * 2 * tpt > tpt ? Places{kPairItem, kPairTile} : Places{kSplitItem, kSplitTile};
+}
+__device__ __forceinline__ int item_places(const Seq& q, const Places& w) {
+  return w.front + w.each * q.tiles;
+}
+__device__ __forceinline__ long long head_places(const Seq& q, int tpt) {
+  if (!q.tiles) return 0;
+  return static_cast<long long>(q.passes - 1) * item_places(q, Places{kPairItem, kPairTile}) +
+         item_places(q, places_of(q, q.passes - 1, tpt));
+}
+// Key tiles of an item that begin before a place of it.
+__device__ __forceinline__ int tiles_before(int place, const Places& w) {
+  return place <= w.front ? 0 : (place - w.front + w.each - 1) / w.each;
 }
 
 // A unit: one CTA's key tiles [tile0, tile0 + nt) of one item; nt 0: no more.
@@ -188,18 +207,25 @@ __device__ __forceinline__ uint32_t visible32(const uint32_t* row, uint2 head, i
   return __funnelshift_r(mask_word(row, head, j, n), mask_word(row, head, j + 1, n), rel & 31);
 }
 
-// OR of `pred` over the `count` threads of a named barrier.
-__device__ __forceinline__ bool barrier_any(int id, int count, bool pred) {
-  uint32_t r;
+// 8 consecutive fp32 columns of this thread's TMEM lane, waits included.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
+  uint32_t r[8];
   asm volatile(
-      "{\n\t.reg .pred q, a;\n\t"
-      "setp.ne.u32 q, %1, 0;\n\t"
-      "bar.red.or.pred a, %2, %3, q;\n\t"
-      "selp.u32 %0, 1, 0, a;\n\t}"
-      : "=r"(r)
-      : "r"(static_cast<uint32_t>(pred)), "r"(id), "r"(count)
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(taddr)
       : "memory");
-  return r != 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n\t"
+      "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+      : "memory");
 }
 
 __device__ __forceinline__ bool nonfinite_pair(uint32_t w) {
@@ -212,7 +238,8 @@ __device__ __forceinline__ bool nonfinite_pair(uint32_t w) {
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_constant__ TreeParams p) {
   using C = Cfg<D>;
-  constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, false, false);
+  // (bit 13 of the instruction descriptor: the first operand is negated)
+  const uint32_t idesc_s = idesc_bf16_f32(128, 64, false, false) | (p.scale_log2 < 0.f ? 1u << 13 : 0u);
   constexpr uint32_t kIdescO = idesc_bf16_f32(128, D, false, true);
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t sbase = smem_u32(smem);
@@ -224,10 +251,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
   uint64_t* kv_empty = kv_full + C::kSlots;
   uint64_t* u_full = kv_empty + C::kSlots;
   uint64_t* u_empty = u_full + kUnits;
-  uint64_t* s_full = u_empty + kUnits;  // per stream: scores ready
-  uint64_t* p_full = s_full + 2;        // weights written back
-  uint64_t* pv_done = p_full + 2;       // P.V complete
-  uint64_t* o_free = pv_done + 2;       // both accumulators of a unit read out
+  uint64_t* s_full = u_empty + kUnits;  // [stream][half]: scores ready
+  uint64_t* p_full = s_full + 4;        // weights written back
+  uint64_t* pv_done = p_full + 4;       // P.V complete
+  uint64_t* o_free = pv_done + 4;       // both accumulators of a unit read out
   uint64_t* drain = o_free + 1;         // per stream
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
@@ -236,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
   // loaded pages of key tile t, in slot t % kMaskRing
   volatile uint32_t* kmask = reinterpret_cast<volatile uint32_t*>(smem + C::kOffMask);
   // drafted tokens of a tile whose V is not finite: [set: stream 0, stream 1,
-  // both][in turn][64-dim half][key / 32]
+  // both][in turn][key / 32]
   volatile uint32_t* poison_s = reinterpret_cast<volatile uint32_t*>(smem + C::kOffPoison);
   static_assert(C::kOffUnit % 16 == 0 && C::kOffMisc % 8 == 0, "alignment of the words");
 
@@ -261,13 +288,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
       mbar_init(&u_full[i], 1);
       mbar_init(&u_empty[i], kUnitReaders);
     }
-    for (int h = 0; h < 2; ++h) {
-      mbar_init(&s_full[h], 1);
-      mbar_init(&p_full[h], 8);  // one arrival per warp of the stream
-      mbar_init(&pv_done[h], 1);
-      mbar_init(&drain[h], 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);  // one arrival per warp of the stream
+      mbar_init(&pv_done[i], 1);
     }
-    mbar_init(o_free, 16);
+    mbar_init(&drain[0], 1);
+    mbar_init(&drain[1], 1);
+    mbar_init(o_free, 8);
     *abort_flag = 0;
     prefetch_tmap(&p.tm_k);
     prefetch_tmap(&p.tm_v);
@@ -286,7 +314,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
     const int s_lo = min(tid * per, p.num_seqs), s_hi = min(s_lo + per, p.num_seqs);
     long long mine = 0;
     for (int s = s_lo; s < s_hi; ++s)
-      mine += seq_places(decode_seq(p, fetch_seq(p, s), blockIdx.x == 0 ? p.err : nullptr), p.hkv);
+      mine += p.hkv * head_places(decode_seq(p, fetch_seq(p, s), blockIdx.x == 0 ? p.err : nullptr),
+                                  p.tpt);
     const long long before = cta_scan<kThreads / 32>(mine, warp_sum, total);
     chunk = (total + gridDim.x - 1) / gridDim.x;
     if (chunk < kMinPlaces) chunk = kMinPlaces;
@@ -294,7 +323,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
     if (begin >= before && begin < before + mine) {
       long long at = begin - before;
       for (int s = s_lo; s < s_hi; ++s) {
-        const long long places = seq_places(decode_seq(p, fetch_seq(p, s), nullptr), p.hkv);
+        const long long places =
+            p.hkv * head_places(decode_seq(p, fetch_seq(p, s), nullptr), p.tpt);
         if (at < places) {
           *plan_seq = s;
           *plan_at = at;
@@ -357,18 +387,20 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
     if (left > 0) {
       s = *plan_seq;
       enter(fetch_seq(p, s));
-      const long long in = *plan_at;
-      const long long item = in / item_places(cur);
-      place = static_cast<int>(in - item * item_places(cur));
-      g = static_cast<int>(item / cur.passes);
-      rp = static_cast<int>(item % cur.passes);
+      const long long in = *plan_at, head = head_places(cur, p.tpt);
+      g = static_cast<int>(in / head);
+      const long long rest = in - g * head;
+      const int whole = item_places(cur, Places{kPairItem, kPairTile});
+      rp = static_cast<int>(min(rest / whole, static_cast<long long>(cur.passes - 1)));
+      place = static_cast<int>(rest - static_cast<long long>(rp) * whole);
     }
     while (true) {
       UnitWords w = {};
       while (left > 0) {  // the next stretch of places with a key tile among them
-        const int all = item_places(cur);
+        const Places w_of = places_of(cur, rp, p.tpt);
+        const int all = item_places(cur, w_of), each = w_of.each;
         const int take = left < all - place ? static_cast<int>(left) : all - place;
-        const int t0 = max(0, place - kItemCost), t1 = max(0, place + take - kItemCost);
+        const int t0 = tiles_before(place, w_of), t1 = tiles_before(place + take, w_of);
         w.s = s;
         w.g = g;
         w.rp = rp;
@@ -379,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
         w.nt = t1 - t0;
         w.tiles = cur.tiles;
         if (t0 == 0 && t1 > 0 && t1 < cur.tiles)  // ends in a later CTA
-          border = make_int4(s, g, rp, static_cast<int>((at - place + all - 1) / chunk));
+          border = make_int4(s, g, rp, static_cast<int>((at - place + all - each) / chunk));
         left -= take;
         at += take;
         place += take;
@@ -432,6 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
         mbar_wait(&q_full[w % kQSlots], (w / kQSlots) & 1, nullptr, p.err);
   } else if (warp == 0) {
     // ======================== K and V producer ========================
+    const uint32_t ubase = __shfl_sync(0xffffffffu, sbase, 0);
     uint32_t pos = 0, kt = 0;
     int slot = 0;
     uint32_t phase = 0;
@@ -455,9 +488,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
           raise_error(p.err, PA_DEV_ERR_BLOCK_ID);
           pb = -1;
         }
-        const bool get = wanted && pb >= 0;
-        const unsigned vm = __ballot_sync(0xffffffffu, get);
+        const unsigned vm = __ballot_sync(0xffffffffu, wanted && pb >= 0);
         const int row = (pb * p.hkv + u.g) * 16;
+        int y[8];
+#pragma unroll
+        for (int pg = 0; pg < 8; ++pg) y[pg] = __shfl_sync(0xffffffffu, row, pg);
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
           mbar_wait(&kv_empty[slot], phase ^ 1, abort_flag, p.err);
@@ -467,19 +502,25 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
               mbar_arrive_expect_tx(&kv_full[slot], __popc(vm) * C::kPage);
             }
             __syncwarp();
-            if (get) {
-              const uint32_t dst = sbase + C::kOffKV + slot * C::kTileBytes;
-              if (v == 0) {  // K half by half, 128 rows each
-                tma_load_2d(dst + lane * 2048, &p.tm_k, 0, row, &kv_full[slot]);
-                if (D == 128)
-                  tma_load_2d(dst + kRegion + lane * 2048, &p.tm_k, 64, row, &kv_full[slot]);
-              } else {  // V page by page, its halves next to each other
-                if (D == 128)
-                  tma_load_3d(dst + lane * C::kPage, &p.tm_v, 0, row, 0, &kv_full[slot]);
-                else
-                  tma_load_2d(dst + lane * C::kPage, &p.tm_v, 0, row, &kv_full[slot]);
+            const uint32_t dst = ubase + C::kOffKV + slot * C::kTileBytes;
+            if (elect_one()) {
+#pragma unroll
+              for (int pg = 0; pg < 8; ++pg) {
+                if ((vm >> pg) & 1u) {
+                  if (v == 0) {  // K half by half, 128 rows each
+                    tma_load_2d(dst + pg * 2048, &p.tm_k, 0, y[pg], &kv_full[slot]);
+                    if (D == 128)
+                      tma_load_2d(dst + kRegion + pg * 2048, &p.tm_k, 64, y[pg], &kv_full[slot]);
+                  } else {  // V page by page, its halves next to each other
+                    if (D == 128)
+                      tma_load_3d(dst + pg * C::kPage, &p.tm_v, 0, y[pg], 0, &kv_full[slot]);
+                    else
+                      tma_load_2d(dst + pg * C::kPage, &p.tm_v, 0, y[pg], &kv_full[slot]);
+                  }
+                }
               }
             }
+            __syncwarp();
             ++pos;
           }
           if (++slot == C::kSlots) {
@@ -494,10 +535,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
         mbar_wait(&kv_full[w % C::kSlots], (w / C::kSlots) & 1, nullptr, p.err);
   } else if (warp < 3) {
     // ============================= MMA ==============================
-    // Warp 1 + h issues stream h's products: the scores of a step, then, when its
-    // weights are written, P.V, then the next step's scores once that has read
-    // them.  The whole warp goes along with the same values and one lane issues,
-    // so the descriptors stay in uniform registers.
+    // Warp 1 + h issues stream h's products.  Step x (half x % 2 of the stream's
+    // tile x / 2) is scored when the P.V of step x - 2 has read its weights:
+    //     S(0), S(1), P.V(0), S(2), P.V(1), S(3), ...
+    // The whole warp goes along with the same values and one lane issues, so the
+    // descriptors stay in uniform registers.
     const int h = warp - 1;
     const uint32_t ubase = __shfl_sync(0xffffffffu, sbase, 0);
     const uint32_t utmem = __shfl_sync(0xffffffffu, tmem, 0);
@@ -505,68 +547,86 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
     const uint64_t dk0 = smem_desc_sw128(ubase + C::kOffKV, 16, 1024);
     const uint64_t dv0 = smem_desc_sw128(ubase + C::kOffKV, 2048, 1024);
     const uint32_t s_col = utmem + h * 128, o_col = utmem + kOCol + h * 128;
-    uint32_t cnt = 0;   // this stream's steps
+    uint32_t cnt = 0;   // this stream's tiles before the unit
     uint32_t qi = 0, unit = 0, kt0 = 0;
     while (next_unit()) {
       const bool pair = __shfl_sync(0xffffffffu, u.pair ? 1 : 0, 0);
       const int nt = __shfl_sync(0xffffffffu, u.nt, 0);
-      const int steps = pair ? nt : (nt - h + 1) >> 1;
+      const int tiles = pair ? nt : (nt - h + 1) >> 1;
       // in pair mode both streams read a K or V slot, and one a q slot; in split
       // mode the other way round: either way two arrivals free it
       const bool kv_twice = !pair, q_twice = pair || nt == 1;
       const uint32_t qq = pair ? qi + h : qi;
       const int qs = qq % kQSlots;
       const uint64_t qa = desc_add(dq0, qs * C::kTileBytes);
-      if (steps > 0)
-        mbar_wait(&q_full[qs], (qq / kQSlots) & 1, abort_flag, p.err);
-      else  // (every unit's, so its parity is never taken for another's)
-        mbar_wait(o_free, (unit & 1) ^ 1, abort_flag, p.err);
-      for (int k = 0; k < steps; ++k, ++cnt) {
-        const uint32_t kpos = 2 * (kt0 + (pair ? k : 2 * k + h));
-        const int ks = kpos % C::kSlots, vs = (kpos + 1) % C::kSlots;
-        mbar_wait(&kv_full[ks], (kpos / C::kSlots) & 1, abort_flag, p.err);
-        // scores replace the weights of the stream's last step: its P.V is done
-        mbar_wait(&pv_done[h], (cnt & 1) ^ 1, abort_flag, p.err);
-        if (__any_sync(0xffffffffu, *abort_flag)) continue;
+      auto position = [&](int x) -> uint32_t {  // ring position of a step's K
+        return 2 * (kt0 + (pair ? x >> 1 : 2 * (x >> 1) + h));
+      };
+      auto scores = [&](int x) {
+        const int half = x & 1;
+        const uint32_t kpos = position(x);
+        const int ks = kpos % C::kSlots;
+        if (half == 0) mbar_wait(&kv_full[ks], (kpos / C::kSlots) & 1, abort_flag, p.err);
+        // the buffer's last weights are read: P.V of step x - 2
+        mbar_wait(&pv_done[2 * h + half], ((cnt + (x >> 1)) & 1) ^ 1, abort_flag, p.err);
+        if (__any_sync(0xffffffffu, *abort_flag)) return;
         tc_fence_after();
-        const uint64_t kb = desc_add(dk0, ks * C::kTileBytes);
+        const uint64_t kb = desc_add(dk0, ks * C::kTileBytes + half * 8192);
         if (elect_one()) {
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
             const uint32_t off = (i >> 2) * kRegion + (i & 3) * 32;
-            umma_ss(s_col, desc_add(qa, off), desc_add(kb, off), kIdescS, i > 0 ? 1u : 0u);
+            umma_ss(s_col + 64 * half, desc_add(qa, off), desc_add(kb, off), idesc_s,
+                    i > 0 ? 1u : 0u);
           }
-          umma_commit(&s_full[h]);
-          umma_commit(&kv_empty[ks]);
-          if (kv_twice) umma_commit(&kv_empty[ks]);
-          if (k == steps - 1) {
+          umma_commit(&s_full[2 * h + half]);
+          if (half) {
+            umma_commit(&kv_empty[ks]);
+            if (kv_twice) umma_commit(&kv_empty[ks]);
+          }
+          if (x == 2 * tiles - 1) {
             umma_commit(&q_empty[qs]);
             if (q_twice) umma_commit(&q_empty[qs]);
           }
         }
         __syncwarp();
-        mbar_wait(&kv_full[vs], ((kpos + 1) / C::kSlots) & 1, abort_flag, p.err);
-        if (k == 0) mbar_wait(o_free, (unit & 1) ^ 1, abort_flag, p.err);
-        mbar_wait(&p_full[h], cnt & 1, abort_flag, p.err);
+      };
+      if (tiles > 0) {
+        mbar_wait(&q_full[qs], (qq / kQSlots) & 1, abort_flag, p.err);
+        scores(0);
+        scores(1);
+      }
+      // (every unit's, so its parity is never taken for another's)
+      mbar_wait(o_free, (unit & 1) ^ 1, abort_flag, p.err);
+      for (int x = 0; x < 2 * tiles; ++x) {
+        const int half = x & 1;
+        const uint32_t vpos = position(x) + 1;
+        const int vs = vpos % C::kSlots;
+        if (half == 0) mbar_wait(&kv_full[vs], (vpos / C::kSlots) & 1, abort_flag, p.err);
+        mbar_wait(&p_full[2 * h + half], (cnt + (x >> 1)) & 1, abort_flag, p.err);
         if (__any_sync(0xffffffffu, *abort_flag)) continue;
         tc_fence_after();
-        const uint64_t vb = desc_add(dv0, vs * C::kTileBytes);
+        const uint64_t vb = desc_add(dv0, vs * C::kTileBytes + half * 4 * C::kPage);
+        const uint32_t pc = s_col + 64 * half;
         if (elect_one()) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            umma_ts(o_col, s_col + 32 * (i >> 1) + 8 * (i & 1), desc_add(vb, i * C::kPage),
-                    kIdescO, k == 0 && i == 0 ? 0u : 1u);
+          for (int i = 0; i < 4; ++i)
+            umma_ts(o_col, pc + 16 * i, desc_add(vb, i * C::kPage), kIdescO,
+                    x == 0 && i == 0 ? 0u : 1u);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            umma_ts(o_col, s_col + 32 * (i >> 1) + 8 * (i & 1) + 16, desc_add(vb, i * C::kPage),
-                    kIdescO, 1u);
-          umma_commit(&pv_done[h]);
-          umma_commit(&kv_empty[vs]);
-          if (kv_twice) umma_commit(&kv_empty[vs]);
+          for (int i = 0; i < 4; ++i)
+            umma_ts(o_col, pc + 16 * i + 8, desc_add(vb, i * C::kPage), kIdescO, 1u);
+          umma_commit(&pv_done[2 * h + half]);
+          if (half) {
+            umma_commit(&kv_empty[vs]);
+            if (kv_twice) umma_commit(&kv_empty[vs]);
+          }
         }
         __syncwarp();
+        if (x + 2 < 2 * tiles) scores(x + 2);
       }
       qi += pair ? 2 : 1;
+      cnt += tiles;
       ++unit;
       kt0 += nt;
     }
@@ -575,176 +635,177 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
     mbar_wait(&drain[h], 0, nullptr, p.err);
   } else {
     // ============================ softmax ============================
-    const int wg = (warp - 4) >> 2;
-    const int h = wg >> 1;     // stream
-    const int half = wg & 1;   // keys 64 half .. of every tile
+    const int h = (warp - 4) >> 2;  // stream
     const int q4 = warp & 3;
     const int r = q4 * 32 + lane;  // row of the tile, TMEM lane
     const uint32_t lane_addr = static_cast<uint32_t>(q4 * 32) << 16;
-    const uint32_t scol = tmem + lane_addr + h * 128 + 64 * half;
+    const uint32_t srow = tmem + lane_addr + h * 128;
     const uint32_t ocol = tmem + lane_addr + kOCol + h * 128;
     const int ti = r / p.group;  // token of this row within its tile
-    // a scale of 0 becomes the smallest there is, which keeps infinities
-    const float sc = p.scale_log2 == 0.f ? 1.2e-38f : p.scale_log2;
-    const float unseen = sc > 0.f ? -CUDART_INF_F : CUDART_INF_F;
+    // (a negative scale's sign is in the scores; 0 becomes the smallest number there
+    // is, which keeps infinities)
+    const float sc = p.scale_log2 == 0.f ? 1.2e-38f : fabsf(p.scale_log2);
     const float2 sc2 = make_float2(sc, sc);
     const float2 neg1 = make_float2(-1.f, -1.f);
-    float* x_own = xbuf + (2 * h + half) * 128 + r;
-    float* x_other = xbuf + (2 * h + (half ^ 1)) * 128 + r;
-    uint32_t cnt = 0;  // this stream's steps
+    uint32_t cnt = 0;  // this stream's tiles
     uint32_t kt0 = 0;  // ring number of the unit's first tile
     // Tail tiles so far: two records of them are in use in turn, so one is only
     // written again when everybody has passed the other's barrier.
     uint32_t split_tails = 0, pair_tails = 0;
-    while (next_unit()) {
-      const int i0 = u.i0 + (u.pair ? h * p.tpt : 0);
-      const bool row_ok = r < rows_box && i0 + ti < u.n;
+    while (true) {
+      // (the unit's slot is kept to the unit's end, and what is seldom needed is
+      // read there when it is: the registers are the scores')
+      const int slot = u_at % kUnits;
+      if (!ring_wait(&u_full[slot], (u_at / kUnits) & 1, p.err)) break;
+      const volatile UnitWords* U = &units[slot];
+      const int nt = U->nt;
+      if (nt == 0) break;
+      ++u_at;
+      const int n = U->n, c = U->L - n, tile0 = U->tile0;
+      const int pass0 = U->rp * 2 * p.tpt;
+      const bool pair = n - pass0 > p.tpt;
+      const int token = pass0 + (pair ? h * p.tpt : 0) + ti;  // this row's, in its sequence
+      const bool row_ok = r < rows_box && token < n;
       const bool warp_ok = __any_sync(0xffffffffu, row_ok);
-      const uint32_t* mrow = p.mask + static_cast<int64_t>(u.q0 + i0 + ti) * p.mask_words;
+      // the row's first mask words, on their way long before they are needed
+      const uint32_t* mrow = p.mask + static_cast<int64_t>(U->q0 + token) * p.mask_words;
       uint2 mhead = make_uint2(0, 0);
       if (row_ok) {
         mhead.x = __ldg(mrow);
-        if (u.n > 32) mhead.y = __ldg(mrow + 1);
+        if (n > 32) mhead.y = __ldg(mrow + 1);
       }
-      const int steps = u.pair ? u.nt : (u.nt - h + 1) >> 1;
+      const int tiles = pair ? nt : (nt - h + 1) >> 1;
       float m = -CUDART_INF_F, l = 0.f;
       bool bad = false;  // this row sees a drafted token whose V is not finite
-      for (int k = 0; k < steps; ++k, ++cnt) {
-        const int tl = u.pair ? k : 2 * k + h;
+#pragma unroll 1
+      for (int x = 0; x < 2 * tiles; ++x) {
+        const int half = x & 1;
+        const int tl = pair ? x >> 1 : 2 * (x >> 1) + h;
         const uint32_t kt = kt0 + tl;
-        const int kv0 = (u.tile0 + tl) * 128;
-        mbar_wait(&s_full[h], cnt & 1, abort_flag, p.err);
+        const int kv0 = (tile0 + tl) * 128 + 64 * half;  // the step's first key
+        const uint32_t scol = srow + 64 * half;
+        mbar_wait(&s_full[2 * h + half], (cnt + (x >> 1)) & 1, abort_flag, p.err);
         tc_fence_after();
-        const uint32_t vm = kmask[kt % kMaskRing];
-        // A tail tile holds drafted tokens or the context's end (the lengths alone
-        // say so: all warps take its barrier, or none).  Any other tile whose
-        // pages were all loaded is whole: every row sees every key.
-        const bool tail = kv0 + 128 > u.c;
-        const bool whole = !tail && vm == 0xffu;
-        uint32_t vis[2] = {0xffffffffu, 0xffffffffu};
-        if (!whole) {
+        const uint32_t vm = (kmask[kt % kMaskRing] >> (4 * half)) & 15u;
+        // A tail step holds drafted tokens or the context's end (the lengths alone
+        // say so: all warps take its barrier, or none).  In any other step whose
+        // pages were all loaded every row sees every key.
+        const bool tail = kv0 + 64 > c;
+        if (tail || vm != 15u) {
+          const int L = U->L;
           volatile uint32_t* pw =
-              poison_s + ((u.pair ? 4 : 2 * h) + ((u.pair ? pair_tails : split_tails) & 1)) * 8;
-          if (!u.pair || h == 0) {
-            // Thread (half, r) looks after that 64-dim half of key row r of V:
-            // zero past the context and in pages that were not loaded (their
-            // weights are 0, and 0 times what is there could be NaN), and zero,
-            // on record, where a drafted token's V is not finite (rows that do
-            // not see it have weight 0).
-            const int key = kv0 + r;
+              poison_s + ((pair ? 4 : 2 * h) + ((pair ? pair_tails : split_tails) & 1)) * 4;
+          // (in pair mode stream 0 does, behind the barrier, and both do where there
+          // is none: the same zeros)
+          if (!pair || h == 0 || !tail) {
+            // Two threads look after a key row of V, a 64-dim half each: zero past
+            // the context and in pages that were not loaded (their weights are 0,
+            // and 0 times what is there could be NaN), and zero, on record, where
+            // a drafted token's V is not finite (rows that do not see it have
+            // weight 0).
+            const int kr = r & 63, part = r >> 6;
+            const int key = kv0 + kr;
             const uint32_t vpos = 2 * kt + 1;
             const int vs = vpos % C::kSlots;
             mbar_wait(&kv_full[vs], (vpos / C::kSlots) & 1, abort_flag, p.err);
-            const bool dead = key >= u.L || !((vm >> (r >> 4)) & 1u);
-            const uint32_t vrow = sbase + C::kOffKV + vs * C::kTileBytes + (r >> 4) * C::kPage +
-                                  half * 2048 + (r & 15) * 128;
+            const bool dead = key >= L || !((vm >> (kr >> 4)) & 1u);
+            const uint32_t vrow = sbase + C::kOffKV + vs * C::kTileBytes +
+                                  (4 * half + (kr >> 4)) * C::kPage + part * 2048 + (kr & 15) * 128;
             bool odd = false;
-            if (half < C::kHalves) {
-              if (!dead && key >= u.c) {
-#pragma unroll 4
+            if (part < C::kHalves) {
+              if (!dead && key >= c) {
+#pragma unroll 2
                 for (int j = 0; j < 8; ++j) {
-                  const uint4 x = lds128(vrow + j * 16);
-                  odd |= nonfinite_pair(x.x) | nonfinite_pair(x.y) | nonfinite_pair(x.z) |
-                         nonfinite_pair(x.w);
+                  const uint4 y = lds128(vrow + j * 16);
+                  odd |= nonfinite_pair(y.x) | nonfinite_pair(y.y) | nonfinite_pair(y.z) |
+                         nonfinite_pair(y.w);
                 }
               }
               if (dead || odd) {
-#pragma unroll 4
+#pragma unroll 2
                 for (int j = 0; j < 8; ++j) sts128_zero(vrow + j * 16);
                 fence_proxy_async_smem();
               }
             }
             const uint32_t word = __ballot_sync(0xffffffffu, odd);
-            if (tail && lane == 0) pw[half * 4 + q4] = word;
+            if (tail && lane == 0) pw[q4] = word;  // [64-dim half][key / 32]
           }
           if (tail) {
-            named_bar_sync(u.pair ? kBarBoth : kBarStream + h, u.pair ? 512 : 256);
-            if (u.pair)
+            named_bar_sync(pair ? kBarBoth : kBarStream + h, pair ? 256 : 128);
+            if (pair)
               ++pair_tails;
             else
               ++split_tails;
           }
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const uint32_t two = vm >> (4 * half + 2 * j);
-            const uint32_t pages = ((two & 1u) ? 0x0000ffffu : 0u) | ((two & 2u) ? 0xffff0000u : 0u);
-            vis[j] = row_ok ? visible32(mrow, mhead, kv0 + 64 * half + 32 * j - u.c, u.n) & pages : 0u;
-            if (tail) bad |= (vis[j] & (pw[2 * half + j] | pw[4 + 2 * half + j])) != 0;
-          }
-        }
-        // Scores of keys that are not seen become infinite in place, of the sign
-        // that scales to -inf: from here on every tile is alike.  (Loops of 32
-        // columns, not unrolled: the hot code of 20 warps in different roles has
-        // to fit the instruction caches.)
-        if (!whole && warp_ok) {
+          // Scores of keys that are not seen become -inf in place: from here on
+          // every step is alike.
+          if (warp_ok) {
 #pragma unroll 1
-          for (int j = 0; j < 2; ++j) {
-            float x[32];
-            tmem_ld32(scol + 32 * j, x);
-            uint32_t w[32];
-            const uint32_t v = j ? vis[1] : vis[0];
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t two = vm >> (2 * j);
+              const uint32_t pages =
+                  ((two & 1u) ? 0x0000ffffu : 0u) | ((two & 2u) ? 0xffff0000u : 0u);
+              const uint32_t vis = row_ok ? visible32(mrow, mhead, kv0 + 32 * j - c, n) & pages : 0u;
+              if (tail) bad |= (vis & (pw[j] | pw[2 + j])) != 0;
+              if (__any_sync(0xffffffffu, row_ok && vis != 0xffffffffu)) {
+                float y[32];
+                tmem_ld32(scol + 32 * j, y);
+                uint32_t w[32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(((v >> i) & 1u) ? x[i] : unseen);
-            tmem_st32_nowait(scol + 32 * j, w);
-          }
-          tmem_wait_st();
-        }
-        // The maximum of this thread's 64 scores (scaled).
-        float top = -CUDART_INF_F;
-        if (warp_ok) {
-#pragma unroll 1
-          for (int j = 0; j < 2; ++j) {
-            float x[32];
-            tmem_ld32(scol + 32 * j, x);
-            float mx[2] = {-CUDART_INF_F, -CUDART_INF_F};
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const float2 y = __fmul2_rn(make_float2(x[i], x[i + 1]), sc2);
-              mx[(i >> 1) & 1] = fmaxf(mx[(i >> 1) & 1], fmaxf(y.x, y.y));
+                for (int i = 0; i < 32; ++i)
+                  w[i] = __float_as_uint(((vis >> i) & 1u) ? y[i] : -CUDART_INF_F);
+                tmem_st32_nowait(scol + 32 * j, w);
+              }
             }
-            top = fmaxf(top, fmaxf(mx[0], mx[1]));
-          }
-        }
-        // The maximum in use is raised (and O_h and l rescaled) only when a tile's
-        // exceeds it by 2^16: weights up to that cannot overflow fp32 sums, and
-        // the division by l makes the result exact either way.
-        const bool want = m == -CUDART_INF_F ? top != -CUDART_INF_F : top > m + kRaiseLog2;
-        if (barrier_any(kBarPair + 4 * h + q4, 64, want && row_ok)) {
-          *x_own = top;
-          named_bar_sync(kBarPair + 4 * h + q4, 64);
-          const float t = fmaxf(top, *x_other);
-          const bool raise = m == -CUDART_INF_F ? t != -CUDART_INF_F : t > m + kRaiseLog2;
-          const float f = !raise ? 1.f : m == -CUDART_INF_F ? 0.f : exp2f(m - t);
-          if (raise) m = t;
-          l *= f;
-          // the stream's last P.V is done: this step's scores came after it
-          if (k > 0 && __any_sync(0xffffffffu, f != 1.f)) {
-#pragma unroll 1
-            for (int cc = 0; cc < D / 32; ++cc) {  // this half's D/2 columns
-              const uint32_t col = ocol + half * (D / 2) + cc * 16;
-              float ov[16];
-              tmem_ld16(col, ov);
-              uint32_t ow[16];
-#pragma unroll
-              for (int i = 0; i < 16; ++i) ow[i] = __float_as_uint(ov[i] * f);
-              tmem_st16(col, ow);
-            }
+            tmem_wait_st();
           }
         }
         if (warp_ok) {
-          // Weights, in place of the scores: per 32 keys 16 columns of P_hi and
-          // 16 of P_lo.
+          // The row's scores and their maximum (scaled).
+          float s[64];
+          tmem_ld64(scol, s);
+          float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+          for (int i = 4; i < 60; i += 8)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) mx[j] = fmaxf(fmaxf(mx[j], s[i + j]), s[i + 4 + j]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], s[60 + j]);
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+          // The maximum in use is raised (and the row of O_h and l rescaled) only
+          // when the step's exceeds it by 2^16: weights up to that cannot overflow
+          // fp32 sums, and the division by l makes the result exact either way.
+          const bool raise = m == -CUDART_INF_F ? top != -CUDART_INF_F : top > m + kRaiseLog2;
+          if (__any_sync(0xffffffffu, raise)) {
+            const float f = !raise ? 1.f : m == -CUDART_INF_F ? 0.f : exp2f(m - top);
+            if (raise) m = top;
+            l *= f;
+            if (x > 0) {  // once the P.V of the step before is done
+              mbar_wait(&pv_done[2 * h + (half ^ 1)], (cnt + ((x - 1) >> 1)) & 1, abort_flag, p.err);
+              tc_fence_after();
+#pragma unroll 1
+              for (int cc = 0; cc < D / 8; ++cc) {
+                float ov[8];
+                tmem_ld8(ocol + cc * 8, ov);
+                uint32_t ow[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) ow[i] = __float_as_uint(ov[i] * f);
+                tmem_st8(ocol + cc * 8, ow);
+              }
+            }
+          }
+          // Weights, in place of the scores: per 16 keys 8 columns of P_hi and 8 of
+          // P_lo.
           const float nm = m == -CUDART_INF_F ? 0.f : -m;
           const float2 nm2 = make_float2(nm, nm);
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll 1
-          for (int j = 0; j < 2; ++j) {
-            float x[32];
-            tmem_ld32(scol + 32 * j, x);
-            uint32_t w[32];
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const float2 y = __ffma2_rn(make_float2(x[i], x[i + 1]), sc2, nm2);
+          for (int j = 0; j < 4; ++j) {
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              const float2 y =
+                  __ffma2_rn(make_float2(s[16 * j + i], s[16 * j + i + 1]), sc2, nm2);
               const float2 e = make_float2(exp2f(y.x), exp2f(y.y));
               sum[(i >> 1) & 1] = __fadd2_rn(sum[(i >> 1) & 1], e);
               const uint32_t ex = __float_as_uint(e.x), ey = __float_as_uint(e.y);
@@ -752,36 +813,30 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
               const float2 hi = make_float2(__uint_as_float(ex & 0xffff0000u),
                                             __uint_as_float(ey & 0xffff0000u));
               const float2 lo = __ffma2_rn(hi, neg1, e);  // e - P_hi, exact
-              w[16 + (i >> 1)] = __byte_perm(__float_as_uint(lo.x), __float_as_uint(lo.y), 0x7632);
+              w[8 + (i >> 1)] = __byte_perm(__float_as_uint(lo.x), __float_as_uint(lo.y), 0x7632);
             }
-            tmem_st32_nowait(scol + 32 * j, w);
+            tmem_st16_nowait(scol + 16 * j, w);
           }
-          tmem_wait_st();
           l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+          tmem_wait_st();
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[h]);
+        if (lane == 0) mbar_arrive(&p_full[2 * h + half]);
       }
+      cnt += tiles;
 
-      // End of the unit: this row's output and log-sum-exp of the unit's keys.  The
-      // sums of a row's two halves meet first (a sum's sign is set where the row
-      // is bad), then, in split mode, the two streams' maxima and sums.
-      if (steps > 0) mbar_wait(&pv_done[h], (cnt - 1) & 1, abort_flag, p.err);
-      tc_fence_before();
-      const int bar = u.pair ? kBarStream + h : kBarBoth, bar_threads = u.pair ? 256 : 512;
-      // (behind the exchange of the last step's maxima, if there was one)
-      named_bar_sync(bar, bar_threads);
-      *x_own = bad ? -l : l;
-      named_bar_sync(bar, bar_threads);
-      const float l_other = *x_other;
-      bad |= signbit(l_other);
-      l += fabsf(l_other);
+      // End of the unit: this row's output and log-sum-exp of the unit's keys.  In
+      // split mode the two streams' maxima and sums (a sum's sign is set where the
+      // row is bad) meet first.
+      // (the last step's P.V: it and all before it are done)
+      if (tiles > 0) mbar_wait(&pv_done[2 * h + 1], (cnt - 1) & 1, abort_flag, p.err);
       float m0 = m, l0 = l, m1 = -CUDART_INF_F, l1 = 0.f;
-      if (!u.pair) {
-        named_bar_sync(kBarBoth, 512);
-        *x_own = half == 0 ? m : bad ? -l : l;  // [stream][0: m, 1: l]
-        named_bar_sync(kBarBoth, 512);
+      if (!pair) {
+        tc_fence_before();
+        xbuf[256 * h + r] = m;  // [stream][m, l][row]
+        xbuf[256 * h + 128 + r] = bad ? -l : l;
+        named_bar_sync(kBarBoth, 256);
         m0 = xbuf[r];
         l0 = xbuf[128 + r];
         m1 = xbuf[256 + r];
@@ -789,7 +844,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
         bad = signbit(l0) | signbit(l1);
         l0 = fabsf(l0);
         l1 = fabsf(l1);
-        named_bar_sync(kBarBoth, 512);  // read by all before either stream writes again
+        named_bar_sync(kBarBoth, 256);  // read by all before either stream writes again
       }
       tc_fence_after();
       const float M = fmaxf(m0, m1);
@@ -800,17 +855,19 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
       const bool live = !(L == 0.f);
       const float inv = bad ? CUDART_NAN_F : live ? 1.f / L : 0.f;
       const float f0 = e0 * inv, f1 = e1 * inv;
-      const bool full = u.nt == u.tiles;
-      const int64_t orow =
-          static_cast<int64_t>(u.q0 + i0 + ti) * p.hq + u.g * p.group + (r - ti * p.group);
-      const int64_t prow = static_cast<int64_t>(2 * blockIdx.x + (u.tile0 == 0 ? 1 : 0)) *
-                               p.part_rows + (u.pair ? h * 128 : 0) + r;
-      // pair mode: this half's D/2 dims of the stream's row; split mode: a quarter
-      // of the dims, from both accumulators
-      const int d0 = u.pair ? half * (D / 2) : wg * (D / 4);
-      const int dims = u.pair ? D / 2 : D / 4;
-      const uint32_t src = (u.pair ? ocol : tmem + lane_addr + kOCol) + d0;
-      const bool two = !u.pair && u.nt > 1;  // stream 1 had a tile
+      const bool full = nt == U->tiles;
+      const int64_t orow = static_cast<int64_t>(U->q0 + token) * p.hq + U->g * p.group +
+                           (r - ti * p.group);
+      const int64_t prow = static_cast<int64_t>(2 * blockIdx.x + (tile0 == 0 ? 1 : 0)) *
+                               p.part_rows + (pair ? h * 128 : 0) + r;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&u_empty[slot]);
+      // pair mode: all dims of the stream's row; split mode: this stream's half of
+      // the dims, from both accumulators
+      const int d0 = pair ? 0 : h * (D / 2);
+      const int dims = pair ? D : D / 2;
+      const uint32_t src = pair ? ocol : tmem + lane_addr + kOCol + d0;
+      const bool two = !pair && nt > 1;  // stream 1 had a tile
       if (warp_ok) {
 #pragma unroll 1
         for (int cc = 0; cc < dims; cc += 16) {
@@ -844,14 +901,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(o_free);
-      if (row_ok && half == 0 && (u.pair || h == 0)) {
+      if (row_ok && (pair || h == 0)) {
         const float lse2 = live ? M + log2f(L) : -CUDART_INF_F;
         if (!full)
           p.part_lse[prow] = lse2;
         else if (p.lse)
           p.lse[orow] = live ? lse2 * kLn2 : -CUDART_INF_F;
       }
-      kt0 += u.nt;
+      kt0 += nt;
     }
   }
 

@@ -282,3 +282,31 @@ def test_graph_replay_and_two_streams():
     o2, _ = pa().pa_tree_attention(**d2, stream=s2)
     torch.cuda.synchronize()
     assert torch.equal(o1, want1[0]) and torch.equal(o2, want2[0])
+
+
+def test_bad_block_in_the_middle_of_two_row_tiles():
+    # a lost block among the cached tokens: both row tiles leave its tokens out,
+    # whatever lay in shared memory where its V would be
+    b = Batch(61, [700, 900], [40, 33], 16, 2, 128)
+    dev = b.device()
+    tables = b.lay.block_tables.copy()
+    tables[0, 10] = b.lay.num_blocks
+    tables[1, 0] = -1
+    dev["block_tables"] = H.dev_i32(tables)
+    poison = H.dev_bf16(np.full_like(b.kp, synth.BF16_NAN))  # leaves NaN in the SMs
+    pa().pa_tree_attention(**{**b.device(), "k_pool": poison, "v_pool": poison})
+    out, lse = pa().pa_tree_attention(**dev, want_lse=True)
+    assert pa().pa_get_device_error() == pa().PA_DEV_ERR_BLOCK_ID
+    from oracle import bf16_bits_to_f64, gather_kv, attend
+    for s, r0, lost in ((0, 0, range(160, 176)), (1, 40, range(0, 16))):
+        L, n = int(b.lay.context_lens[s]), int(b.n[s])
+        K, V = gather_kv(b.kp, b.vp, b.lay.block_tables[s], L)
+        for i in (0, 5, n - 1):
+            see = [t for t in drafting._visible(b.mask[r0 + i], L - n, n) if t not in lost]
+            for h in range(16):
+                o, e = attend(bf16_bits_to_f64(b.h["q"][r0 + i, h]),
+                              bf16_bits_to_f64(K[h // 8])[see], bf16_bits_to_f64(V[h // 8])[see],
+                              b.lay.scale)
+                assert abs(float(lse[r0 + i, h]) - e) <= 2e-5 + 1e-6 * abs(e)
+                d = np.abs(H.host_f64(out[r0 + i, h]) - o)
+                assert np.all(d <= 2.0 ** -8 * np.abs(o) + 3e-4)
