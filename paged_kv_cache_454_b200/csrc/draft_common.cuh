@@ -6,9 +6,11 @@
 
 namespace pa {
 
+// (Not the read-only path: what is read here may have been written by a kernel that
+// still ran when this one was set up.)
 __device__ __forceinline__ int ld_i32(const int32_t* ptr) {
   int x;
-  asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(x) : "l"(ptr));
+  asm volatile("ld.global.b32 %0, [%1];" : "=r"(x) : "l"(ptr));
   return x;
 }
 
@@ -41,6 +43,14 @@ struct SeqRaw {
   int q0, q1, L;
 };
 
+// Quotient of two non-negative numbers; a 64-bit division is ten times a 32-bit
+// one, and the numbers here rarely need it.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  if (((a | b) >> 32) == 0)
+    return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 // Exclusive scan of one number per thread over a CTA of `warps` warps (`slots`: as
 // many words of shared memory); `total` is the sum of all.
 template <int kWarps>
@@ -61,6 +71,26 @@ __device__ __forceinline__ long long cta_scan(long long mine, long long* slots, 
     total += slots[w];
   }
   return before;
+}
+
+// Launch of a kernel that may be set up while the one before it on the stream ends
+// (it waits for that one's end itself, before it reads anything).
+template <typename P>
+inline int launch_overlapped(void (*kernel)(P), dim3 grid, int threads, int smem, const P& p,
+                             cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess) return PA_OK;
+  cudaGetLastError();
+  return PA_ERR_CUDA;
 }
 
 }  // namespace pa

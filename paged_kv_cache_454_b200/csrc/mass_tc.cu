@@ -57,9 +57,9 @@ struct Cfg {
   static constexpr int kOffUnit = kOffLse + kQSlots * 128 * 4;
   static constexpr int kOffBar = kOffUnit + kUnits * 32;
   static constexpr int kNumBars = 2 * kQSlots + 2 * kSlots + 2 * kUnits + 2 * kUnitTiles + 1;
-  // tensor-memory slot, abort flag, plan {sequence, place in it (8 bytes)}
+  // tensor-memory slot, abort flag, plan (five words, then 8 bytes)
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
-  static constexpr int kOffMask = kOffMisc + 24;
+  static constexpr int kOffMask = kOffMisc + 40;
   static constexpr int kOffScan = (kOffMask + 4 * kMaskRing + 7) / 8 * 8;
   static constexpr int kSmem = kOffScan + kThreads / 32 * 8;
   static_assert(kSmem <= 232448, "shared memory per CTA");
@@ -166,8 +166,9 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
   uint64_t* drain = s_free + kUnitTiles;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
-  volatile int* plan_seq = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8);
-  volatile long long* plan_at = reinterpret_cast<volatile long long*>(smem + C::kOffMisc + 16);
+  // where this CTA begins: sequence, its q0, q1 and length, head; place in the head
+  volatile int* plan = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8);
+  volatile long long* plan_at = reinterpret_cast<volatile long long*>(smem + C::kOffMisc + 32);
   volatile uint32_t* kmask = reinterpret_cast<volatile uint32_t*>(smem + C::kOffMask);
   static_assert(C::kOffMisc % 8 == 0 && C::kOffUnit % 16 == 0, "alignment of the words");
 
@@ -198,6 +199,12 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
     prefetch_tmap(&p.tm_k);
     prefetch_tmap(&p.tm_q);
   }
+  // This kernel may have been set up while the one before it ran, and reads nothing
+  // before that one's end.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (warp == 1) tmem_alloc(tmem_slot, kTmemCols);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
   // Where this CTA's stretch begins: as in the tree kernel, a scan over the
   // threads' runs of sequences.
   long long chunk, total;
@@ -205,29 +212,39 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
     const int per = (p.num_seqs + kThreads - 1) / kThreads;
     const int s_lo = min(tid * per, p.num_seqs), s_hi = min(s_lo + per, p.num_seqs);
     long long mine = 0;
-    for (int s = s_lo; s < s_hi; ++s)
-      mine += p.hkv * head_places(decode_seq(p, fetch_seq(p, s), blockIdx.x == 0 ? p.err : nullptr),
-                                  p.tpt);
+    SeqRaw raw = {};
+    Seq q = {};
+    for (int s = s_lo; s < s_hi; ++s) {
+      raw = fetch_seq(p, s);
+      q = decode_seq(p, raw, blockIdx.x == 0 ? p.err : nullptr);
+      mine += p.hkv * head_places(q, p.tpt);
+    }
     const long long before = cta_scan<kThreads / 32>(
         mine, reinterpret_cast<long long*>(smem + C::kOffScan), total);
-    chunk = (total + gridDim.x - 1) / gridDim.x;
+    chunk = quotient(total + gridDim.x - 1, gridDim.x);
     if (chunk < 1) chunk = 1;
     const long long begin = chunk * blockIdx.x;
     if (begin >= before && begin < before + mine) {
       long long at = begin - before;
-      for (int s = s_lo; s < s_hi; ++s) {
-        const long long places =
-            p.hkv * head_places(decode_seq(p, fetch_seq(p, s), nullptr), p.tpt);
-        if (at < places) {
-          *plan_seq = s;
-          *plan_at = at;
-          break;
+      int s = s_lo;
+      if (per > 1)
+        for (; s < s_hi; ++s) {
+          raw = fetch_seq(p, s);
+          q = decode_seq(p, raw, nullptr);
+          const long long places = p.hkv * head_places(q, p.tpt);
+          if (at < places) break;
+          at -= places;
         }
-        at -= places;
-      }
+      const long long head = head_places(q, p.tpt);
+      const int g = static_cast<int>(quotient(at, head));
+      plan[0] = s;
+      plan[1] = raw.q0;
+      plan[2] = raw.q1;
+      plan[3] = raw.L;
+      plan[4] = g;
+      *plan_at = at - g * head;
     }
   }
-  if (warp == 1) tmem_alloc(tmem_slot, kTmemCols);
   fence_barrier_init();
   tc_fence_before();
   __syncthreads();
@@ -280,14 +297,12 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
       left = 0;  // past the last sequence
     };
     if (left > 0) {
-      s = *plan_seq;
-      enter(fetch_seq(p, s));
-      const long long head = head_places(cur, p.tpt);
-      const long long in = *plan_at;
-      g = static_cast<int>(in / head);
-      long long at = in - g * head;  // the first tile whose first place is at or past this
+      s = plan[0];
+      enter(SeqRaw{plan[1], plan[2], plan[3]});
+      g = plan[4];
+      long long at = *plan_at;  // the first tile whose first place is at or past this
       const int each = max(1, cur.cols), full = full_tiles(cur, p.tpt);
-      const long long whole = min(static_cast<long long>(full), (at + each - 1) / each);
+      const long long whole = min(static_cast<long long>(full), quotient(at + each - 1, each));
       j = static_cast<int>(whole);
       at -= whole * each;  // places before tile j that belong to the CTA before: at <= 0
       while (at > 0 && j < cur.tiles) at -= tile_places(cur, j++, p.tpt);
@@ -372,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
           float e = CUDART_INF_F;
           if (c < cols) {
             const int64_t row = q.q0 + static_cast<int64_t>(i) * p.tpt + c / p.group;
-            e = __ldg(p.lse + row * p.hq + u.g * p.group + c % p.group);
+            e = p.lse[row * p.hq + u.g * p.group + c % p.group];
             e = e == -CUDART_INF_F ? CUDART_INF_F : e * kLog2e;
           }
           lse_s[qs * 128 + c] = e;
@@ -540,9 +555,8 @@ int launch_mass(MassParams& p, const void* q, int64_t q_stride, const void* k_po
                           Cfg<D>::kSmem) < 1)
     return PA_ERR_CUDA;
   const int64_t sms = num_sms();
-  mass_tc_kernel<D><<<static_cast<int>(most_tiles < sms ? most_tiles : sms), kThreads,
-                      Cfg<D>::kSmem, stream>>>(p);
-  return launch_status();
+  return launch_overlapped(mass_tc_kernel<D>, dim3(static_cast<int>(most_tiles < sms ? most_tiles : sms)),
+                           kThreads, Cfg<D>::kSmem, p, stream);
 }
 
 }  // namespace

@@ -89,9 +89,9 @@ struct Cfg {
   static constexpr int kOffX = kOffUnit + kUnits * 48;  // [4][128] floats: exchanges of a row
   static constexpr int kOffBar = kOffX + 4 * 128 * 4;
   static constexpr int kNumBars = 2 * kQSlots + 2 * kSlots + 2 * kUnits + 12 + 3;
-  // tensor-memory slot, abort flag, plan {sequence, place in it (8 bytes)}
+  // tensor-memory slot, abort flag, plan (seven words)
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
-  static constexpr int kOffMask = kOffMisc + 24;
+  static constexpr int kOffMask = kOffMisc + 40;
   static constexpr int kOffPoison = kOffMask + 4 * kMaskRing;  // [3 sets][2][4 words]
   static constexpr int kSmem = kOffPoison + 3 * 2 * 16;
   static_assert(kSmem <= 232448, "shared memory per CTA");
@@ -199,7 +199,7 @@ __device__ __forceinline__ uint32_t mask_word(const uint32_t* row, uint2 head, i
   if (j < 0) return 0xffffffffu;
   const int have = n - 32 * j;
   if (have <= 0) return 0;
-  const uint32_t w = j == 0 ? head.x : j == 1 ? head.y : __ldg(row + j);
+  const uint32_t w = j == 0 ? head.x : j == 1 ? head.y : row[j];
   return have >= 32 ? w : w & ((1u << have) - 1u);
 }
 __device__ __forceinline__ uint32_t visible32(const uint32_t* row, uint2 head, int rel, int n) {
@@ -226,6 +226,29 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8])
       "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
       : "memory");
+}
+
+// Transposes, within every four lanes, the 4 x 4 16-byte words that are v[0..3] of
+// each: lane j's v[i] becomes lane i's v[j].
+__device__ __forceinline__ void transpose4(uint4 (&v)[4], int lane) {
+#pragma unroll
+  for (int b = 1; b <= 2; b <<= 1) {
+    const bool up = lane & b;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k & b) continue;
+      const uint4 x = up ? v[k] : v[k | b];
+      uint4 y;
+      y.x = __shfl_xor_sync(0xffffffffu, x.x, b);
+      y.y = __shfl_xor_sync(0xffffffffu, x.y, b);
+      y.z = __shfl_xor_sync(0xffffffffu, x.z, b);
+      y.w = __shfl_xor_sync(0xffffffffu, x.w, b);
+      if (up)
+        v[k] = y;
+      else
+        v[k | b] = y;
+    }
+  }
 }
 
 __device__ __forceinline__ bool nonfinite_pair(uint32_t w) {
@@ -258,8 +281,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
   uint64_t* drain = o_free + 1;         // per stream
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
-  volatile int* plan_seq = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8);
-  volatile long long* plan_at = reinterpret_cast<volatile long long*>(smem + C::kOffMisc + 16);
+  // where this CTA begins: sequence, its q0, q1 and length, head, pass, place
+  volatile int* plan = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8);
   // loaded pages of key tile t, in slot t % kMaskRing
   volatile uint32_t* kmask = reinterpret_cast<volatile uint32_t*>(smem + C::kOffMask);
   // drafted tokens of a tile whose V is not finite: [set: stream 0, stream 1,
@@ -269,6 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (sbase & 1023u) {  // the swizzled tiles need it, and the compiler gives it
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (tid == 0) {
       raise_error(p.err, PA_DEV_ERR_TIMEOUT);
       p.border[blockIdx.x] = make_int4(-1, 0, 0, 0);
@@ -301,40 +325,58 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
     prefetch_tmap(&p.tm_v);
     prefetch_tmap(&p.tm_q);
   }
-  // the merge kernel may be set up now (it waits for this grid's end)
+  // The merge kernel may be set up now (it waits for this grid's end); this one may
+  // have been while the kernel before it ran, and reads nothing before that one's
+  // end.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (warp == 1) tmem_alloc(tmem_slot, kTmemCols);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // Where this CTA's stretch begins.  Thread i sums a run of sequences, a scan
   // over the threads places the runs on the line, and the thread whose run holds
   // the CTA's first place finds it there.
   long long chunk, total;
   {
-    long long* warp_sum = reinterpret_cast<long long*>(xbuf);
     const int per = (p.num_seqs + kThreads - 1) / kThreads;
     const int s_lo = min(tid * per, p.num_seqs), s_hi = min(s_lo + per, p.num_seqs);
     long long mine = 0;
-    for (int s = s_lo; s < s_hi; ++s)
-      mine += p.hkv * head_places(decode_seq(p, fetch_seq(p, s), blockIdx.x == 0 ? p.err : nullptr),
-                                  p.tpt);
-    const long long before = cta_scan<kThreads / 32>(mine, warp_sum, total);
-    chunk = (total + gridDim.x - 1) / gridDim.x;
+    SeqRaw raw = {};
+    Seq q = {};
+    for (int s = s_lo; s < s_hi; ++s) {
+      raw = fetch_seq(p, s);
+      q = decode_seq(p, raw, blockIdx.x == 0 ? p.err : nullptr);
+      mine += p.hkv * head_places(q, p.tpt);
+    }
+    const long long before =
+        cta_scan<kThreads / 32>(mine, reinterpret_cast<long long*>(xbuf), total);
+    chunk = quotient(total + gridDim.x - 1, gridDim.x);
     if (chunk < kMinPlaces) chunk = kMinPlaces;
     const long long begin = chunk * blockIdx.x;
     if (begin >= before && begin < before + mine) {
       long long at = begin - before;
-      for (int s = s_lo; s < s_hi; ++s) {
-        const long long places =
-            p.hkv * head_places(decode_seq(p, fetch_seq(p, s), nullptr), p.tpt);
-        if (at < places) {
-          *plan_seq = s;
-          *plan_at = at;
-          break;
+      int s = s_lo;
+      if (per > 1)
+        for (; s < s_hi; ++s) {
+          raw = fetch_seq(p, s);
+          q = decode_seq(p, raw, nullptr);
+          const long long places = p.hkv * head_places(q, p.tpt);
+          if (at < places) break;
+          at -= places;
         }
-        at -= places;
-      }
+      const long long head = head_places(q, p.tpt);
+      const int g = static_cast<int>(quotient(at, head));
+      const long long rest = at - g * head;
+      const int whole = item_places(q, Places{kPairItem, kPairTile});
+      const int rp = static_cast<int>(min(quotient(rest, whole), static_cast<long long>(q.passes - 1)));
+      plan[0] = s;
+      plan[1] = raw.q0;
+      plan[2] = raw.q1;
+      plan[3] = raw.L;
+      plan[4] = g;
+      plan[5] = rp;
+      plan[6] = static_cast<int>(rest - static_cast<long long>(rp) * whole);
     }
   }
-  if (warp == 1) tmem_alloc(tmem_slot, kTmemCols);
   fence_barrier_init();
   tc_fence_before();
   __syncthreads();
@@ -385,14 +427,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
       if (s + 1 < p.num_seqs) next = fetch_seq(p, s + 1);
     };
     if (left > 0) {
-      s = *plan_seq;
-      enter(fetch_seq(p, s));
-      const long long in = *plan_at, head = head_places(cur, p.tpt);
-      g = static_cast<int>(in / head);
-      const long long rest = in - g * head;
-      const int whole = item_places(cur, Places{kPairItem, kPairTile});
-      rp = static_cast<int>(min(rest / whole, static_cast<long long>(cur.passes - 1)));
-      place = static_cast<int>(rest - static_cast<long long>(rp) * whole);
+      s = plan[0];
+      enter(SeqRaw{plan[1], plan[2], plan[3]});
+      g = plan[4];
+      rp = plan[5];
+      place = plan[6];
     }
     while (true) {
       UnitWords w = {};
@@ -411,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
         w.nt = t1 - t0;
         w.tiles = cur.tiles;
         if (t0 == 0 && t1 > 0 && t1 < cur.tiles)  // ends in a later CTA
-          border = make_int4(s, g, rp, static_cast<int>((at - place + all - each) / chunk));
+          border = make_int4(s, g, rp, static_cast<int>(quotient(at - place + all - each, chunk)));
         left -= take;
         at += take;
         place += take;
@@ -671,8 +710,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
       const uint32_t* mrow = p.mask + static_cast<int64_t>(U->q0 + token) * p.mask_words;
       uint2 mhead = make_uint2(0, 0);
       if (row_ok) {
-        mhead.x = __ldg(mrow);
-        if (n > 32) mhead.y = __ldg(mrow + 1);
+        mhead.x = mrow[0];
+        if (n > 32) mhead.y = mrow[1];
       }
       const int tiles = pair ? nt : (nt - h + 1) >> 1;
       float m = -CUDART_INF_F, l = 0.f;
@@ -868,7 +907,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
       const int dims = pair ? D : D / 2;
       const uint32_t src = pair ? ocol : tmem + lane_addr + kOCol + d0;
       const bool two = !pair && nt > 1;  // stream 1 had a tile
-      if (warp_ok) {
+      // (nothing seen: the accumulator of all-zero weights is zero, and stays so)
+      if (warp_ok && full) {
 #pragma unroll 1
         for (int cc = 0; cc < dims; cc += 16) {
           float a[16];
@@ -881,8 +921,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
 #pragma unroll
             for (int i = 0; i < 16; ++i) a[i] = fmaf(b[i], f1, a[i]);
           }
-          // nothing seen: the accumulator of all-zero weights is zero, and stays so
-          if (row_ok && full) {
+          if (row_ok) {
             uint4* dst = reinterpret_cast<uint4*>(p.out + orow * D + d0 + cc);
 #pragma unroll
             for (int i = 0; i < 2; ++i)
@@ -890,12 +929,35 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
                                   pack_bf16x2(a[8 * i + 2], a[8 * i + 3]),
                                   pack_bf16x2(a[8 * i + 4], a[8 * i + 5]),
                                   pack_bf16x2(a[8 * i + 6], a[8 * i + 7]));
-          } else if (row_ok) {
-            float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + d0 + cc);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              dst[i] = make_float4(a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]);
           }
+        }
+      } else if (warp_ok) {
+        // Partial rows, four lanes' transposed before they are stored: a lane then
+        // holds the same 16-byte chunk of four rows, and the lanes' chunks of a row
+        // lie next to each other (a store of 32 rows' chunks takes 32 turns of the
+        // load-store unit, 4000 cycles of a small call in all).
+        const int q = lane & 3;
+        const uint32_t oks = __ballot_sync(0xffffffffu, row_ok) >> (lane & ~3);
+#pragma unroll 1
+        for (int cc = 0; cc < dims; cc += 16) {
+          float a[16];
+          tmem_ld16(src + cc, a);
+          float b[16] = {};
+          if (two) tmem_ld16(src + 128 + cc, b);
+          uint4 v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float y[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[j] = fmaf(b[4 * i + j], two ? f1 : 0.f, a[4 * i + j] * f0);
+            v[i] = make_uint4(__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]),
+                              __float_as_uint(y[3]));
+          }
+          transpose4(v, lane);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if ((oks >> i) & 1u)
+              *reinterpret_cast<uint4*>(p.part_o + (prow - q + i) * D + d0 + cc + 4 * q) = v[i];
         }
       }
       tc_fence_before();
@@ -930,6 +992,7 @@ constexpr int kMergeWarps = 4;
 template <int D>
 __global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(
     const __grid_constant__ TreeParams p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 b = p.border[blockIdx.x];
   if (b.x < 0) return;
@@ -1011,23 +1074,11 @@ int launch_tree(TreeParams& p, const void* q, int64_t q_stride, const void* k_po
     return PA_ERR_CUDA;
   const int sms = num_sms() < kMaxCtas ? num_sms() : kMaxCtas;
   const int grid = static_cast<int>(most_tiles < sms ? most_tiles : sms);
-  tree_tc_kernel<D><<<grid, kThreads, Cfg<D>::kSmem, stream>>>(p);
-  const int st = launch_status();
+  const int st =
+      launch_overlapped(tree_tc_kernel<D>, dim3(grid), kThreads, Cfg<D>::kSmem, p, stream);
   if (st != PA_OK) return st;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, p.part_rows / (2 * kMergeWarps));
-  cfg.blockDim = dim3(32 * kMergeWarps);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, tree_merge_kernel<D>, p) != cudaSuccess) {
-    cudaGetLastError();
-    return PA_ERR_CUDA;
-  }
-  return PA_OK;
+  return launch_overlapped(tree_merge_kernel<D>, dim3(grid, p.part_rows / (2 * kMergeWarps)),
+                           32 * kMergeWarps, 0, p, stream);
 }
 
 }  // namespace
