@@ -43,6 +43,24 @@ struct SeqRaw {
   int q0, q1, L;
 };
 
+// Division by a number from 1 to 256 that the host knows, of numbers below 2^24: the
+// product with m = floor(2^32 / d) + 1 exceeds n 2^32 / d by less than n, hence the
+// quotient by less than 2^-8 <= 1/d.
+struct Divisor {
+  uint64_t m;
+  Divisor() = default;
+  explicit Divisor(uint32_t d) : m((1ull << 32) / d + 1) {}
+  __device__ __forceinline__ int quotient(uint32_t n) const {
+    return static_cast<int>((n * m) >> 32);
+  }
+};
+
+__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+               "r"(bytes)
+               : "memory");
+}
+
 // Quotient of two non-negative numbers; a 64-bit division is ten times a 32-bit
 // one, and the numbers here rarely need it.
 __device__ __forceinline__ long long quotient(long long a, long long b) {

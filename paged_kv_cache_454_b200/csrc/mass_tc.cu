@@ -14,10 +14,11 @@
 // Work split: a key tile costs as many places as column tiles look at it (a
 // causal chunk's later keys are seen by fewer), and the places of all key tiles,
 // in order, are cut into equal stretches, one per CTA; a key tile belongs to the
-// stretch that holds its first place.  A unit is up to four neighbouring key
+// stretch that holds its first place.  A unit is four, two or one neighbouring key
 // tiles, which share each column tile's load: their K tiles stay in shared memory
-// while the q tiles stream by, and each has its own scores in tensor memory and
-// its own warpgroup.
+// while the q tiles stream by (two at most where there are several column tiles,
+// so that the next unit's K arrives meanwhile).  Key tile t of a CTA belongs to
+// warpgroup t % 4 and its quarter of tensor memory.
 //
 // Bound: HBM for a few queries (K once); for many the exponentials (128 keys x
 // 128 columns are 1024 cycles of an SM's multi-function units, 512 of its tensor
@@ -39,7 +40,7 @@ using namespace tc;
 
 constexpr int kThreads = 640;
 constexpr int kRegion = 128 * 128;
-constexpr int kQSlots = 2;
+constexpr int kQSlots = 3;
 constexpr int kUnits = 4;
 constexpr int kUnitTiles = 4;          // key tiles of a unit at most
 constexpr int kUnitReaders = 3 + 16;   // K, MMA, q, warpgroup warps
@@ -50,7 +51,7 @@ template <int D>
 struct Cfg {
   static constexpr int kHalves = D / 64;
   static constexpr int kTileBytes = kHalves * kRegion;
-  static constexpr int kSlots = D == 128 ? 5 : 9;  // K ring
+  static constexpr int kSlots = D == 128 ? 4 : 9;  // K ring
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = kQSlots * kTileBytes;
   static constexpr int kOffLse = kOffK + kSlots * kTileBytes;  // [kQSlots][128]
@@ -84,9 +85,15 @@ struct __align__(64) MassParams {
   int hq;
   int group;
   int tpt;  // queries of a column tile
+  Divisor by_tpt, by_group;
   int num_seqs;
   float scale_log2;
 };
+
+__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n)
+               : "memory");
+}
 
 struct Seq {
   int q0, n, L;
@@ -115,29 +122,30 @@ __device__ __forceinline__ Seq decode_seq(const MassParams& p, const SeqRaw& r, 
   if (!ok && err) raise_error(err, PA_DEV_ERR_CONTEXT);
   if (!ok || r.L == 0) return q;
   q.tiles = (r.L + 127) >> 7;
-  q.cols = (q.n + p.tpt - 1) / p.tpt;
+  q.cols = p.by_tpt.quotient(q.n + p.tpt - 1);
   return q;
 }
 
 // Column tiles whose queries all lie before key tile j: they do not see it.
-__device__ __forceinline__ int first_cols(const Seq& q, int j, int tpt) {
+__device__ __forceinline__ int first_cols(const MassParams& p, const Seq& q, int j) {
   const int rel = j * 128 - (q.L - q.n);
-  return rel <= 0 ? 0 : rel / tpt;
+  return rel <= 0 ? 0 : p.by_tpt.quotient(rel);
 }
 // Places of a key tile (one for a tile that no query of the step sees: its sums
 // are copied all the same) and of a head.
-__device__ __forceinline__ int tile_places(const Seq& q, int j, int tpt) {
-  return max(1, q.cols - first_cols(q, j, tpt));
+__device__ __forceinline__ int tile_places(const MassParams& p, const Seq& q, int j) {
+  return max(1, q.cols - first_cols(p, q, j));
 }
 // Key tiles that every column tile sees.
-__device__ __forceinline__ int full_tiles(const Seq& q, int tpt) {
-  return min(q.tiles, (q.L - q.n + tpt - 1) / 128 + 1);
+__device__ __forceinline__ int full_tiles(const MassParams& p, const Seq& q) {
+  return min(q.tiles, (q.L - q.n + p.tpt - 1) / 128 + 1);
 }
-__device__ __forceinline__ long long head_places(const Seq& q, int tpt) {
+__device__ __forceinline__ long long head_places(const MassParams& p, const Seq& q) {
   if (!q.tiles) return 0;
-  const int full = full_tiles(q, tpt);
+  const int full = full_tiles(p, q);
   long long sum = static_cast<long long>(full) * max(1, q.cols);
-  for (int j = full; j < q.tiles; ++j) sum += tile_places(q, j, tpt);
+#pragma unroll 1
+  for (int j = full; j < q.tiles; ++j) sum += tile_places(p, q, j);
   return sum;
 }
 
@@ -174,13 +182,14 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (sbase & 1023u) {  // the swizzled tiles need it, and the compiler gives it
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (tid == 0) raise_error(p.err, PA_DEV_ERR_TIMEOUT);
     return;
   }
   if (tid == 0) {
     for (int i = 0; i < kQSlots; ++i) {
       mbar_init(&q_full[i], 1);
-      mbar_init(&q_empty[i], 1 + 16);  // the MMAs, and every warpgroup warp (the lse)
+      mbar_init(&q_empty[i], 1 + 16);  // the MMAs; the lse's readers: 4 nj warps, 4 / nj each
     }
     for (int i = 0; i < C::kSlots; ++i) {
       mbar_init(&k_full[i], 1);
@@ -200,10 +209,9 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
     prefetch_tmap(&p.tm_q);
   }
   // This kernel may have been set up while the one before it ran, and reads nothing
-  // before that one's end.
+  // but the lengths before that one's end.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp == 1) tmem_alloc(tmem_slot, kTmemCols);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // Where this CTA's stretch begins: as in the tree kernel, a scan over the
   // threads' runs of sequences.
@@ -217,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
     for (int s = s_lo; s < s_hi; ++s) {
       raw = fetch_seq(p, s);
       q = decode_seq(p, raw, blockIdx.x == 0 ? p.err : nullptr);
-      mine += p.hkv * head_places(q, p.tpt);
+      mine += p.hkv * head_places(p, q);
     }
     const long long before = cta_scan<kThreads / 32>(
         mine, reinterpret_cast<long long*>(smem + C::kOffScan), total);
@@ -231,11 +239,11 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
         for (; s < s_hi; ++s) {
           raw = fetch_seq(p, s);
           q = decode_seq(p, raw, nullptr);
-          const long long places = p.hkv * head_places(q, p.tpt);
+          const long long places = p.hkv * head_places(p, q);
           if (at < places) break;
           at -= places;
         }
-      const long long head = head_places(q, p.tpt);
+      const long long head = head_places(p, q);
       const int g = static_cast<int>(quotient(at, head));
       plan[0] = s;
       plan[1] = raw.q0;
@@ -247,6 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
   }
   fence_barrier_init();
   tc_fence_before();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
@@ -269,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
     q.n = u.n;
     q.L = u.L;
     q.tiles = (u.L + 127) >> 7;
-    q.cols = (u.n + p.tpt - 1) / p.tpt;
+    q.cols = p.by_tpt.quotient(u.n + p.tpt - 1);
     return q;
   };
 
@@ -301,11 +310,11 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
       enter(SeqRaw{plan[1], plan[2], plan[3]});
       g = plan[4];
       long long at = *plan_at;  // the first tile whose first place is at or past this
-      const int each = max(1, cur.cols), full = full_tiles(cur, p.tpt);
+      const int each = max(1, cur.cols), full = full_tiles(p, cur);
       const long long whole = min(static_cast<long long>(full), quotient(at + each - 1, each));
       j = static_cast<int>(whole);
       at -= whole * each;  // places before tile j that belong to the CTA before: at <= 0
-      while (at > 0 && j < cur.tiles) at -= tile_places(cur, j++, p.tpt);
+      while (at > 0 && j < cur.tiles) at -= tile_places(p, cur, j++);
       left += at;  // the stretch begins -at places later
       if (j >= cur.tiles) next_head();
     }
@@ -318,11 +327,15 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
         w.n = cur.n;
         w.L = cur.L;
         w.j0 = j;
-        while (w.nj < kUnitTiles && j < cur.tiles && left > 0) {
-          left -= tile_places(cur, j, p.tpt);
+        const int most = cur.cols > 1 ? 2 : kUnitTiles;
+        long long taken = 0;  // places of the tiles counted, without the last one's
+        while (w.nj < most && j + w.nj < cur.tiles && taken < left) {
+          taken += tile_places(p, cur, j + w.nj);
           ++w.nj;
-          ++j;
         }
+        if (w.nj == 3) taken -= tile_places(p, cur, j + --w.nj);
+        left -= taken;
+        j += w.nj;
         if (j == cur.tiles && left > 0) next_head();
       }
       const int slot = u_at % kUnits;
@@ -338,14 +351,25 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
   } else if (warp == 0) {
     // ============================ K producer ============================
     uint32_t kt = 0, issued = 0;
-    while (next_unit()) {
-      const int32_t* table = p.block_tables + static_cast<int64_t>(u.s) * p.max_blocks;
-      const int blocks = (u.L + 15) >> 4;
-      const int b = u.j0 * 8 + lane;  // the unit's 32 entries at most
-      const int ent = b < blocks && lane < 8 * u.nj ? ld_i32(table + b) : -1;
-      for (int jj = 0; jj < u.nj; ++jj, ++kt) {
+    // a unit's block-table entries (32 at most) are read while the unit before it
+    // is copied
+    auto entries = [&]() {
+      const int b = u.j0 * 8 + lane;
+      return b < (u.L + 15) >> 4 && lane < 8 * u.nj
+                 ? ld_i32(p.block_tables + static_cast<int64_t>(u.s) * p.max_blocks + b)
+                 : -1;
+    };
+    bool more = next_unit();
+    int ent_next = more ? entries() : -1;
+    while (more) {
+      const UnitWords now = u;
+      const int ent = ent_next;
+      const int blocks = (now.L + 15) >> 4;
+      more = next_unit();
+      if (more) ent_next = entries();
+      for (int jj = 0; jj < now.nj; ++jj, ++kt) {
         int pb = __shfl_sync(0xffffffffu, ent, jj * 8 + (lane & 7));
-        const bool wanted = lane < 8 && (u.j0 + jj) * 8 + lane < blocks;
+        const bool wanted = lane < 8 && (now.j0 + jj) * 8 + lane < blocks;
         if (wanted && (pb < 0 || pb >= p.num_blocks)) {
           raise_error(p.err, PA_DEV_ERR_BLOCK_ID);
           pb = -1;
@@ -361,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
         }
         __syncwarp();
         if (get) {
-          const int row = (pb * p.hkv + u.g) * 16;
+          const int row = (pb * p.hkv + now.g) * 16;
           const uint32_t dst = sbase + C::kOffK + slot * C::kTileBytes + lane * 2048;
           tma_load_2d(dst, &p.tm_k, 0, row, &k_full[slot]);
           if (D == 128) tma_load_2d(dst + kRegion, &p.tm_k, 64, row, &k_full[slot]);
@@ -377,29 +401,33 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
     uint32_t qi = 0, issued = 0;
     while (next_unit()) {
       const Seq q = unit_seq();
-      for (int i = first_cols(q, u.j0, p.tpt); i < q.cols; ++i, ++qi) {
+      for (int i = first_cols(p, q, u.j0); i < q.cols; ++i, ++qi) {
         const int qs = qi % kQSlots;
         mbar_wait(&q_empty[qs], ((qi / kQSlots) & 1) ^ 1, abort_flag, p.err);
         if (__any_sync(0xffffffffu, *abort_flag)) continue;
-        // column c: query i * tpt + c / G, head c % G; +inf: a column that adds nothing
-        const int cols = min(p.tpt, q.n - i * p.tpt) * p.group;
-        for (int c = lane; c < 128; c += 32) {
-          float e = CUDART_INF_F;
-          if (c < cols) {
-            const int64_t row = q.q0 + static_cast<int64_t>(i) * p.tpt + c / p.group;
-            e = p.lse[row * p.hq + u.g * p.group + c % p.group];
-            e = e == -CUDART_INF_F ? CUDART_INF_F : e * kLog2e;
-          }
-          lse_s[qs * 128 + c] = e;
-        }
-        __syncwarp();
         if (lane == 0) {
           const uint32_t dst = sbase + C::kOffQ + qs * C::kTileBytes;
           const int token = q.q0 + i * p.tpt;
-          mbar_arrive_expect_tx(&q_full[qs], C::kHalves * rows_box * 128);
+          mbar_expect_tx(&q_full[qs], C::kHalves * rows_box * 128);
           tma_load_3d(dst, &p.tm_q, 0, u.g * p.group, token, &q_full[qs]);
           if (D == 128) tma_load_3d(dst + kRegion, &p.tm_q, 64, u.g * p.group, token, &q_full[qs]);
         }
+        // column c: query i * tpt + c / G, head c % G; +inf: a column that adds nothing
+        const int cols = min(p.tpt, q.n - i * p.tpt) * p.group;
+        const float* lse = p.lse + (q.q0 + static_cast<int64_t>(i) * p.tpt) * p.hq + u.g * p.group;
+        float e[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int c = lane + 32 * k;
+          const uint32_t query = p.by_group.quotient(c);
+          e[k] = c < cols ? lse[static_cast<int64_t>(query) * p.hq + (c - query * p.group)]
+                          : -CUDART_INF_F;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          lse_s[qs * 128 + lane + 32 * k] = e[k] == -CUDART_INF_F ? CUDART_INF_F : e[k] * kLog2e;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[qs]);
         issued = qi + 1;
       }
     }
@@ -412,11 +440,12 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
     const uint32_t utmem = __shfl_sync(0xffffffffu, tmem, 0);
     const uint64_t dq0 = smem_desc_sw128(ubase + C::kOffQ, 16, 1024);
     const uint64_t dk0 = smem_desc_sw128(ubase + C::kOffK, 16, 1024);
-    uint32_t qi = 0, kt0 = 0, steps[kUnitTiles] = {0, 0, 0, 0};
+    uint32_t qi = 0, kt0 = 0;
+    uint32_t steps = 0;  // bit w: parity of warpgroup w's steps
     while (next_unit()) {
       const Seq q = unit_seq();
       const int nj = __shfl_sync(0xffffffffu, u.nj, 0);
-      const int i0 = first_cols(q, u.j0, p.tpt);
+      const int i0 = first_cols(p, q, u.j0);
       if (i0 >= q.cols)  // no query sees the unit: its K is passed over
         for (int jj = 0; jj < nj; ++jj) {
           const uint32_t kt = kt0 + jj;
@@ -429,29 +458,27 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
         const uint32_t idesc = idesc_bf16_f32(128, (cols + 15) & ~15, false, false);
         const uint64_t qb = desc_add(dq0, qs * C::kTileBytes);
         mbar_wait(&q_full[qs], (qi / kQSlots) & 1, abort_flag, p.err);
+        for (int jj = 0; jj < nj; ++jj) {
+          const uint32_t kt = kt0 + jj;
+          const int slot = kt % C::kSlots, w = kt % kUnitTiles;
+          mbar_wait(&k_full[slot], (kt / C::kSlots) & 1, abort_flag, p.err);
+          mbar_wait(&s_free[w], ((steps >> w) & 1) ^ 1, abort_flag, p.err);
+          steps ^= 1u << w;
+          const bool stop = __any_sync(0xffffffffu, *abort_flag);
+          tc_fence_after();
+          const uint64_t ka = desc_add(dk0, slot * C::kTileBytes);
+          if (!stop && elect_one()) {
 #pragma unroll
-        for (int jj = 0; jj < kUnitTiles; ++jj) {
-          if (jj < nj) {
-            const uint32_t kt = kt0 + jj;
-            const int slot = kt % C::kSlots;
-            mbar_wait(&k_full[slot], (kt / C::kSlots) & 1, abort_flag, p.err);
-            mbar_wait(&s_free[jj], (steps[jj] & 1) ^ 1, abort_flag, p.err);
-            ++steps[jj];
-            tc_fence_after();
-            const uint64_t ka = desc_add(dk0, slot * C::kTileBytes);
-            if (!__any_sync(0xffffffffu, *abort_flag) && elect_one()) {
-#pragma unroll
-              for (int k = 0; k < D / 16; ++k) {
-                const uint32_t off = (k >> 2) * kRegion + (k & 3) * 32;
-                umma_ss(utmem + 128 * jj, desc_add(ka, off), desc_add(qb, off), idesc,
-                        k > 0 ? 1u : 0u);
-              }
-              umma_commit(&s_full[jj]);
-              if (i == q.cols - 1) umma_commit(&k_empty[slot]);
-              if (jj == nj - 1) umma_commit(&q_empty[qs]);
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t off = (k >> 2) * kRegion + (k & 3) * 32;
+              umma_ss(utmem + 128 * w, desc_add(ka, off), desc_add(qb, off), idesc,
+                      k > 0 ? 1u : 0u);
             }
-            __syncwarp();
+            umma_commit(&s_full[w]);
+            if (i == q.cols - 1) umma_commit(&k_empty[slot]);
+            if (jj == nj - 1) umma_commit(&q_empty[qs]);
           }
+          __syncwarp();
         }
       }
       kt0 += nj;
@@ -469,16 +496,14 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
     uint32_t qi = 0, kt0 = 0, steps = 0;
     while (next_unit()) {
       const Seq q = unit_seq();
-      const int i0 = first_cols(q, u.j0, p.tpt);
-      if (wg >= u.nj) {  // no tile: only lets the q slots go, each in its turn
-        for (int i = i0; i < q.cols; ++i, ++qi) {
-          mbar_wait(&q_full[qi % kQSlots], (qi / kQSlots) & 1, abort_flag, p.err);
-          if (lane == 0) mbar_arrive(&q_empty[qi % kQSlots]);
-        }
+      const int i0 = first_cols(p, q, u.j0);
+      const int jj = (wg - kt0) & 3;  // this warpgroup's tile of the unit
+      if (jj >= u.nj) {
+        qi += q.cols - min(i0, q.cols);
         kt0 += u.nj;
         continue;
       }
-      const int key = (u.j0 + wg) * 128 + r;
+      const int key = (u.j0 + jj) * 128 + r;
       const int64_t at = (static_cast<int64_t>(u.s) * p.hkv + u.g) * p.mass_stride + key;
       const float before = p.mass_in && key < q.L ? p.mass_in[at] : 0.f;
       const int rel = key - (q.L - q.n);  // this key among the step's own tokens
@@ -512,13 +537,13 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&s_free[wg]);
-          mbar_arrive(&q_empty[qi % kQSlots]);
+          mbar_arrive_n(&q_empty[qi % kQSlots], 4 / u.nj);
         }
       }
       // (a page that was not loaded: nothing added)
       bool loaded = true;
       if (i0 < q.cols) {
-        loaded = (kmask[(kt0 + wg) % kMaskRing] >> (r >> 4)) & 1u;
+        loaded = (kmask[(kt0 + jj) % kMaskRing] >> (r >> 4)) & 1u;
       }
       if (key < q.L) p.mass_out[at] = before + (loaded ? sum0 + sum1 : 0.f);
       kt0 += u.nj;
@@ -611,6 +636,8 @@ int pa_attention_mass(const void* q, int64_t q_stride, const float* lse, const i
   p.tpt = 128 / group;
   // (a decode step's tile: one query)
   if (max_q_len < p.tpt) p.tpt = max_q_len;
+  p.by_tpt = Divisor(p.tpt);
+  p.by_group = Divisor(group);
   p.num_seqs = num_seqs;
   p.scale_log2 = scale * kLog2e;
   const int64_t tiles = (static_cast<int64_t>(max_blocks_per_seq) * 16 + 127) / 128;

@@ -120,6 +120,7 @@ struct __align__(64) TreeParams {
   int hq;
   int group;
   int tpt;          // tokens of a row tile
+  Divisor by_pass;  // division by 2 tpt
   int num_seqs;
   int part_rows;    // 128 or 256
   float scale_log2;
@@ -152,7 +153,7 @@ __device__ __forceinline__ Seq decode_seq(const TreeParams& p, const SeqRaw& r, 
   if (!ok && err) raise_error(err, PA_DEV_ERR_CONTEXT);
   if (!ok || q.n == 0) return q;
   q.tiles = (r.L + 127) >> 7;
-  q.passes = (q.n + 2 * p.tpt - 1) / (2 * p.tpt);
+  q.passes = p.by_pass.quotient(q.n + 2 * p.tpt - 1);
   return q;
 }
 
@@ -326,11 +327,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
     prefetch_tmap(&p.tm_q);
   }
   // The merge kernel may be set up now (it waits for this grid's end); this one may
-  // have been while the kernel before it ran, and reads nothing before that one's
-  // end.
+  // have been while the kernel before it ran, and reads nothing but the lengths
+  // before that one's end.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp == 1) tmem_alloc(tmem_slot, kTmemCols);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // Where this CTA's stretch begins.  Thread i sums a run of sequences, a scan
   // over the threads places the runs on the line, and the thread whose run holds
@@ -379,6 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
   }
   fence_barrier_init();
   tc_fence_before();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
@@ -1148,6 +1149,7 @@ int pa_tree_attention(const void* q, int64_t q_stride, const int32_t* cu_q_lens,
   p.hq = num_q_heads;
   p.group = group;
   p.tpt = 128 / group;
+  p.by_pass = Divisor(2 * p.tpt);
   p.num_seqs = num_seqs;
   p.part_rows = rows_of(max_q_len, group);
   p.scale_log2 = scale * kLog2e;
