@@ -342,12 +342,15 @@ def _dims(name, t, dims):
 
 
 def _rows_arg(name, t, device, shape=None):
-    """A bf16 [T, H, D] tensor whose heads are packed; returns its token stride."""
+    """A bf16 [T, H, D] tensor whose heads are packed (``shape``: the sizes it must
+    have); returns its token stride."""
     _arg(name, t, _torch().bfloat16, device, shape, contiguous=False)
     if shape is None:
         _dims(name, t, 3)
         shape = t.shape
     tokens, heads, dim = shape
+    if t.is_contiguous():
+        return heads * dim
     stride, by_head, by_dim = t.stride()
     if (by_dim != 1 and dim > 1) or (by_head != dim and heads > 1):
         raise ValueError(f"{name} must be [T, H, D] with packed heads")
@@ -362,20 +365,25 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+_entry_points = {}
+
+
 def _run(name, device, stream, *args):
     """Call ``name`` of the library with the stream's handle as its last argument."""
-    torch = _torch()
-    fn = getattr(_abi.load(), name)
+    fn = _entry_points.get(name)
+    if fn is None:
+        fn = _entry_points[name] = getattr(_abi.load(), name)
+    cuda = _torch()._C
     if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(device.index)
+        handle = cuda._cuda_getCurrentRawStream(device.index)
     else:
         if stream.device != device:
             raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
         handle = stream.cuda_stream
-    if device.index == torch.cuda.current_device():
+    if device.index == cuda._cuda_getDevice():
         status = fn(*args, handle)
     else:
-        with torch.cuda.device(device):
+        with _torch().cuda.device(device):
             status = fn(*args, handle)
     if status:
         _abi.check(name, status)
@@ -487,6 +495,9 @@ def pa_tree_workspace_size(max_q_len, num_q_heads, k_pool) -> int:
                                                   pool_desc(k_pool)))
 
 
+_tree_workspace = {}
+
+
 def pa_tree_attention(q, cu_q_lens, max_q_len, tree_mask, k_pool, v_pool, block_tables,
                       context_lens, scale, out=None, lse=None, workspace=None, stream=None,
                       want_lse=False):
@@ -518,8 +529,11 @@ def pa_tree_attention(q, cu_q_lens, max_q_len, tree_mask, k_pool, v_pool, block_
     elif want_lse:
         lse = _empty((total_q, hq), torch.float32, dev, stream)
     if workspace is None:
-        n = _abi.load().pa_tree_workspace_size(int(max_q_len), hq, desc)
-        workspace = _empty(max(n, 16), torch.uint8, dev, stream)
+        sizes = (int(max_q_len), hq, desc.num_kv_heads, d)
+        n = _tree_workspace.get(sizes)  # (a function of these sizes alone)
+        if n is None:
+            n = _tree_workspace[sizes] = max(pa_tree_workspace_size(max_q_len, hq, k_pool), 16)
+        workspace = _empty(n, torch.uint8, dev, stream)
     else:
         _arg("workspace", workspace, torch.uint8, dev)
     _run("pa_tree_attention", dev, stream, q.data_ptr(), qs, cu_q_lens.data_ptr(), total_q,

@@ -169,21 +169,28 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS)
   for (int k = 0; k < ITEMS; ++k) key[k] = key_of(__uint_as_float(key[k]));
   __syncthreads();  // all weights are read: in place, theirs may be overwritten
   // Tokens kept anyway have their places already; `open`: the others, whose key
-  // counts (a key of 0 reaches no threshold).
-  uint32_t open = 0;
+  // counts (a key of 0 reaches no threshold).  Most warps have none of the former.
+  uint32_t open = 0xffffffffu >> (32 - min(items, 32));
+  if (warp * items * 32 < lo || (warp + 1) * items * 32 > hi) {
+    open = 0;
 #pragma unroll
-  for (int k = 0; k < ITEMS; ++k) {
-    const int t = first + 32 * k;
-    if (k < items && t >= lo && t < hi) {
-      open |= 1u << k;
-    } else {
-      if (k < items && t < c.len) {
-        const int i = t < lo ? t : c.keep - (c.len - t);
-        kept[i] = t;
-        out[i] = weight_of(key[k]);
+    for (int k = 0; k < ITEMS; ++k) {
+      const int t = first + 32 * k;
+      if (k < items && t >= lo && t < hi) {
+        open |= 1u << k;
+      } else {
+        if (k < items && t < c.len) {
+          const int i = t < lo ? t : c.keep - (c.len - t);
+          kept[i] = t;
+          out[i] = weight_of(key[k]);
+        }
+        key[k] = 0;
       }
-      key[k] = 0;
     }
+  } else {
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k)
+      if (k >= items) key[k] = 0;
   }
   if (c.need == 0) return;
   // The largest threshold that at least `need` keys reach.
@@ -530,18 +537,27 @@ __device__ __forceinline__ int move_count(const MoveParams& p, int s, bool flag)
   return n < 0 ? 0 : p.kept_stride;
 }
 
-// Into other blocks: a warp takes eight rows; lanes 0-7 look the rows up, then
-// every row's K and V go as 16-byte chunks, a quarter (D = 64: a half) of the
-// warp's rows in flight at a time.
-constexpr int kMoveThreads = 256;
-constexpr int kMoveRows = 8;                                   // rows of a warp
-constexpr int kMoveCtaRows = kMoveRows * (kMoveThreads / 32);  // of a CTA's turn
+// Into other blocks: a warp takes as many rows as two accesses of 16 bytes a lane
+// cover; their first lanes look them up, then every row's K and V go at once.
+// Measured on 48 sequences brought down to 1531 tokens (602 MB moved): four rows of
+// D = 128 per warp 123 us with the choice, eight 136, sixteen 133; small CTAs (128
+// threads) and many of them (64 per SM) 123, 16 per SM 129; a lane looking up a row
+// each for 32 rows at a time 122, but 24 against 21 us on one long sequence.
+constexpr int kMoveThreads = 128;
+constexpr int kMoveSteps = 2;
+__host__ __device__ constexpr int move_rows(int head_dim) {  // of a warp
+  return kMoveSteps * 32 / (head_dim / 8);
+}
+__host__ __device__ constexpr int move_cta_rows(int head_dim) {
+  return move_rows(head_dim) * (kMoveThreads / 32);
+}
 
 template <int D>
 __global__ void __launch_bounds__(kMoveThreads) move_out_kernel(const __grid_constant__ MoveParams p) {
   constexpr int kLanes = D / 8;           // chunks of a row
   constexpr int kAtOnce = 32 / kLanes;    // rows a warp covers with one access
-  constexpr int kSteps = kMoveRows / kAtOnce;
+  constexpr int kSteps = kMoveSteps;
+  constexpr int kMoveRows = move_rows(D), kMoveCtaRows = move_cta_rows(D);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int sg = blockIdx.x / p.parts, part = blockIdx.x % p.parts;
   const int s = sg / p.hkv, g = sg % p.hkv;
@@ -582,15 +598,16 @@ __global__ void __launch_bounds__(kMoveThreads) move_out_kernel(const __grid_con
 
 // In place: blockIdx.x = ((sequence, head), slice); a slice is four 16-byte
 // chunks of K's or V's rows.  Thread i of a turn takes rows i / 4, + 64, ...
+constexpr int kPlaceThreads = 256;
 constexpr int kSliceLanes = 4;
 constexpr int kPlaceUnroll = 4;
 
 template <int D>
-__global__ void __launch_bounds__(kMoveThreads) move_in_place_kernel(
+__global__ void __launch_bounds__(kPlaceThreads) move_in_place_kernel(
     const __grid_constant__ MoveParams p) {
   constexpr int kRowChunks = D / 8;
   constexpr int kSlices = kRowChunks / kSliceLanes;  // of K, and as many of V
-  constexpr int kRows = kMoveThreads / kSliceLanes;
+  constexpr int kRows = kPlaceThreads / kSliceLanes;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int sg = blockIdx.x / (2 * kSlices), slice = blockIdx.x % (2 * kSlices);
   const int s = sg / p.hkv, g = sg % p.hkv;
@@ -650,7 +667,8 @@ int run_move(MoveParams& p, int head_dim, bool dependent, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(p.num_seqs) * p.hkv;
   if (p.new_tables) {
     // enough CTAs to fill the device several times over, no more than the rows need
-    const int64_t most = (p.kept_stride + kMoveCtaRows - 1) / kMoveCtaRows;
+    const int cta_rows = move_cta_rows(head_dim);
+    const int64_t most = (p.kept_stride + cta_rows - 1) / cta_rows;
     const int64_t want = (static_cast<int64_t>(num_sms()) * 64 + rows - 1) / rows;
     p.parts = static_cast<int>(std::max<int64_t>(1, std::min(most, want)));
     if (rows * p.parts > 0x7fffffff) return PA_ERR_UNSUPPORTED;
@@ -662,9 +680,9 @@ int run_move(MoveParams& p, int head_dim, bool dependent, cudaStream_t stream) {
   const int64_t grid = rows * 2 * (head_dim / 8 / kSliceLanes);
   if (grid > 0x7fffffff) return PA_ERR_UNSUPPORTED;
   return head_dim == 128
-             ? launch_dependent(move_in_place_kernel<128>, static_cast<int>(grid), kMoveThreads, p,
+             ? launch_dependent(move_in_place_kernel<128>, static_cast<int>(grid), kPlaceThreads, p,
                                 dependent, stream)
-             : launch_dependent(move_in_place_kernel<64>, static_cast<int>(grid), kMoveThreads, p,
+             : launch_dependent(move_in_place_kernel<64>, static_cast<int>(grid), kPlaceThreads, p,
                                 dependent, stream);
 }
 
