@@ -44,7 +44,10 @@ constexpr int kQSlots = 3;
 constexpr int kUnits = 4;
 constexpr int kUnitTiles = 4;          // key tiles of a unit at most
 constexpr int kUnitReaders = 3 + 16;   // K, MMA, q, warpgroup warps
-constexpr int kMaskRing = 16;
+// Loaded pages of the key tiles.  A warp that took unit U but not the next keeps the
+// producer within U + kUnits, so its tile's entry stands until it took that one.
+constexpr int kMaskRing = 32;
+static_assert(kMaskRing >= (kUnits + 1) * kUnitTiles, "an entry outlives its unit");
 constexpr uint32_t kTmemCols = 512;    // four tiles of scores
 
 template <int D>

@@ -218,3 +218,25 @@ def test_mass_in_graphs_on_two_streams():
     got = pa().pa_attention_mass(**devs[0], stream=streams[0])
     streams[0].synchronize()
     assert torch.equal(got, want[0])
+
+
+def test_bad_blocks_among_sequences_without_rows():
+    # units whose K is passed over (no rows) let the copies run far ahead of the tiles
+    # still in work: each tile's pages have to stay its own
+    lens = [640, 2100, 70, 1900, 513, 129, 2048, 33] * 6
+    n = [1, 0, 3, 0, 1, 0, 0, 2] * 6
+    for d in (64, 128):
+        b = Batch(41 + d, lens, n, 4, 1, d)
+        dev = b.device()
+        tables = b.lay.block_tables.copy()
+        want = b.want()
+        for s, L in enumerate(lens):
+            if n[s] and s % 3:
+                k = (5 * s) % (-(-L // 16))
+                tables[s, k] = -1
+                want[s][:, 16 * k:16 * k + 16] = 0
+        dev["block_tables"] = H.dev_i32(tables)
+        for _ in range(5):
+            got = pa().pa_attention_mass(**dev)
+            b.check(got, want=want)
+        assert pa().pa_get_device_error() == pa().PA_DEV_ERR_BLOCK_ID
