@@ -79,7 +79,8 @@ PA_API int pa_attention_mass(const void* q, int64_t q_stride, const float* lse,
  *                no block of block_tables in use; a sequence whose blocks other
  *                sequences share must be packed this way.  In place, a sequence's
  *                blocks must be its own.
- *   kept         int32 [num_seqs][num_kv_heads][kept_stride], out.
+ *   kept         int32 [num_seqs][num_kv_heads][kept_stride], out; kept_stride >= 1
+ *                (a budget of 0 empties a sequence).
  *   new_lens     int32 [num_seqs], out; must not be context_lens.
  *   mass_out     float [num_seqs][num_kv_heads][mass_out_stride], out: the kept
  *                tokens' weights, packed alike (-0 becomes 0, a NaN the canonical

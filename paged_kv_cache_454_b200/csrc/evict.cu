@@ -716,7 +716,7 @@ int pa_evict(const float* mass, int64_t mass_stride, void* k_pool, void* v_pool,
   PA_NVTX_RANGE("pa_evict");
   int st = check_pool(pool);
   if (st != PA_OK) return st;
-  if (num_seqs < 0 || max_blocks_per_seq <= 0 || sink < 0 || recent < 0 || kept_stride < 0 ||
+  if (num_seqs < 0 || max_blocks_per_seq <= 0 || sink < 0 || recent < 0 || kept_stride <= 0 ||
       mass_stride < 0 || mass_out_stride < 0)
     return PA_ERR_ARG;
   if (num_seqs == 0) return PA_OK;
@@ -761,7 +761,7 @@ int pa_evict(const float* mass, int64_t mass_stride, void* k_pool, void* v_pool,
     evict_select_long_kernel<<<r, kSelThreads, 0, cs>>>(p);
     st = launch_status();
   }
-  if (st != PA_OK || kept_stride == 0) return st;
+  if (st != PA_OK) return st;
   MoveParams m = {};
   m.k_pool = static_cast<uint4*>(k_pool);
   m.v_pool = static_cast<uint4*>(v_pool);

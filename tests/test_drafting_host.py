@@ -143,6 +143,15 @@ def test_compact_refusals(lib):
     refuse(call, _abi.PA_ERR_UNSUPPORTED, desc=pool(d=32))
 
 
+def test_evict_refuses_a_choice_without_room(lib):
+    # (the choice alone would end with its lengths still on their way: the calls after
+    # it rely on the move's end)
+    other = [ctypes.c_void_p(0x20000 + 0x10000 * i) for i in range(2)]
+    for new, blocks in ((None, 0), (ctypes.c_void_p(0x50000), 4)):
+        assert lib.pa_evict(FAKE, 64, FAKE, FAKE, pool(), FAKE, 4, FAKE, FAKE, 0, 0, new, blocks,
+                            FAKE, 0, other[0], other[1], 8, 2, None) == _abi.PA_ERR_ARG
+
+
 def test_frequencies():
     f, factor = pa.pa_rope_frequencies(8)
     assert factor == 1.0 and np.allclose(f, [1, 0.1, 0.01, 0.001], rtol=1e-15)
