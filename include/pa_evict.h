@@ -108,8 +108,9 @@ PA_API int pa_evict(const float* mass, int64_t mass_stride, void* k_pool, void* 
  *                in place.
  *   base         int32 [num_seqs], device, or NULL for zeros.
  *   kept         int32 [num_seqs][kept_heads][kept_stride]; kept_heads is
- *                num_kv_heads, or 1 for a list all heads share.  Ascending in i
- *                (which makes the move in place independent of its order).
+ *                num_kv_heads, or 1 for a list all heads share.  Strictly ascending
+ *                in i and not below 0 (which makes the move in place independent
+ *                of its order); kept_stride is at most 2^30.
  *   counts       int32 [num_seqs]; beyond [0, kept_stride] they are clamped, with
  *                PA_DEV_ERR_CONTEXT.
  * A row outside its table is left out, with PA_DEV_ERR_CONTEXT.

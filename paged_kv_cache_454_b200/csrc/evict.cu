@@ -795,6 +795,8 @@ int pa_compact_tokens(void* k_pool, void* v_pool, pa_pool_desc pool, const int32
   if (!k_pool || !v_pool || !block_tables || !kept || !counts) return PA_ERR_ARG;
   if (!aligned16(k_pool) || !aligned16(v_pool)) return PA_ERR_ARG;
   if (new_tables && (new_max_blocks <= 0 || new_tables == block_tables)) return PA_ERR_ARG;
+  // a row's number within a list, and a turn's step past it, stay an int
+  if (kept_stride > (1 << 30)) return PA_ERR_UNSUPPORTED;
   MoveParams m = {};
   m.err = device_error_word();
   if (!m.err) return PA_ERR_CUDA;

@@ -152,6 +152,13 @@ def test_evict_refuses_a_choice_without_room(lib):
                             FAKE, 0, other[0], other[1], 8, 2, None) == _abi.PA_ERR_ARG
 
 
+def test_compact_refuses_lists_past_its_row_numbers(lib):
+    # (a turn of the move past 2^30 rows could leave an int)
+    for new, blocks in ((None, 0), (ctypes.c_void_p(0x40000), 4)):
+        assert lib.pa_compact_tokens(FAKE, FAKE, pool(), FAKE, 4, new, blocks, None, FAKE, 2,
+                                     (1 << 30) + 1, FAKE, 2, None) == _abi.PA_ERR_UNSUPPORTED
+
+
 def test_frequencies():
     f, factor = pa.pa_rope_frequencies(8)
     assert factor == 1.0 and np.allclose(f, [1, 0.1, 0.01, 0.001], rtol=1e-15)
