@@ -13,7 +13,7 @@
 // sorting.  A small CTA takes a row of up to 8192 tokens, so that several rows
 // share an SM.  Longer rows, and any where there are few, are shared by a cluster
 // of eight CTAs (evict_select_cluster_kernel): the same steps, two bits at a time,
-// the counts of all warps exchanged through distributed shared memory.  Rows past
+// the counts of all warps sent through distributed shared memory.  Rows past
 // 131072 tokens (evict_select_long_kernel) are read again for every eight bits,
 // with a histogram per warp.
 //
@@ -277,14 +277,37 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS)
 
 // A row shared by a cluster of eight CTAs: lane l's item k of the cluster's warp w
 // is token (w * items + k) * 32 + l.
+//
+// Every warp sends its word of counts to every CTA and waits on an mbarrier of its
+// own CTA for all warps' words: no fence, and no barrier of the cluster, in a step.
+// Measured on 8 rows of 31337 tokens: 13.4 us; with the words stored and a barrier of
+// the cluster in every step 17.8, the fences of those the largest stall.
+// Two sets of words and mbarriers in turn are enough: a warp sends its word of step
+// i + 2 when it has all words of step i + 1, and a warp sent that only after it read
+// the words of step i.  No word is on its way to a CTA that ended: a CTA's last
+// words are the last that are sent.
 constexpr int kSelCluster = 8;
+
+__device__ __forceinline__ uint32_t map_rank(uint32_t addr, int rank) {
+  uint32_t x;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(x) : "r"(addr), "r"(rank));
+  return x;
+}
+__device__ __forceinline__ void send_word(uint32_t dst, uint32_t word, uint32_t bar) {
+  asm volatile(
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(dst),
+      "r"(word), "r"(bar)
+      : "memory");
+}
 
 template <int THREADS, int ITEMS>
 __global__ void __cluster_dims__(kSelCluster, 1, 1) __launch_bounds__(THREADS, 1)
     evict_select_cluster_kernel(const __grid_constant__ SelectParams p) {
   namespace cg = cooperative_groups;
   constexpr int kWarps = THREADS / 32 * kSelCluster;  // of the cluster
-  __shared__ int4 counts[2][kWarps];  // every warp's, in every CTA; in turn
+  static_assert(32 * ITEMS < 1024, "three counts of a warp share a word");
+  __shared__ uint32_t counts[2][kWarps];  // every warp's, in every CTA; in turn
+  __shared__ uint64_t arrived[2];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank());
@@ -302,13 +325,18 @@ __global__ void __cluster_dims__(kSelCluster, 1, 1) __launch_bounds__(THREADS, 1
   const int lo = c.sink, hi = c.len - c.recent;
   int32_t* kept = p.kept + static_cast<int64_t>(row) * p.kept_stride;
   float* out = p.mass_out + row * p.mass_out_stride;
+  if (tid == 0) {
+    mbar_init(&arrived[0], 1);
+    mbar_init(&arrived[1], 1);
+    fence_barrier_init();
+  }
   uint32_t key[ITEMS];
 #pragma unroll
   for (int k = 0; k < ITEMS; ++k)
     key[k] = __float_as_uint(mass[min(first + 32 * min(k, items - 1), c.len - 1)]);
 #pragma unroll
   for (int k = 0; k < ITEMS; ++k) key[k] = key_of(__uint_as_float(key[k]));
-  cluster.sync();  // all weights are read (and all CTAs have started)
+  cluster.sync();  // all weights are read, and all CTAs have their mbarriers
   uint32_t open = 0;
 #pragma unroll
   for (int k = 0; k < ITEMS; ++k) {
@@ -325,13 +353,19 @@ __global__ void __cluster_dims__(kSelCluster, 1, 1) __launch_bounds__(THREADS, 1
     }
   }
   if (c.need == 0) return;
-  // Every warp's numbers in every CTA: lane j of a warp writes CTA j's copy.
+  // Every warp's word in every CTA (lane j sends to CTA j); null after a time-out.
   int turn = 0;
-  auto exchange = [&](int4 mine) -> int4* {
-    int4* slots = counts[turn++ & 1];
-    if (lane < kSelCluster) *cluster.map_shared_rank(&slots[warp], lane) = mine;
-    cluster.sync();
-    return slots;
+  auto exchange = [&](uint32_t mine) -> const uint32_t* {
+    const int set = turn & 1;
+    if (tid == 0) mbar_arrive_expect_tx(&arrived[set], kWarps * 4);
+    if (lane < kSelCluster)
+      send_word(map_rank(smem_u32(&counts[set][warp]), lane), mine,
+                map_rank(smem_u32(&arrived[set]), lane));
+    const bool ok = mbar_wait(&arrived[set], (turn >> 1) & 1, nullptr, p.err);
+    ++turn;
+    if (__all_sync(0xffffffffu, ok)) return counts[set];
+    cluster.sync();  // nobody ends while another may still send
+    return nullptr;
   };
   uint32_t bar = 0;
   int above = hi - lo;
@@ -345,15 +379,15 @@ __global__ void __cluster_dims__(kSelCluster, 1, 1) __launch_bounds__(THREADS, 1
         n2 += key[k] >= cand + (1u << b);
         n3 += key[k] >= cand + (2u << b);
       }
-      n1 = __reduce_add_sync(0xffffffffu, n1);
-      n2 = __reduce_add_sync(0xffffffffu, n2);
-      n3 = __reduce_add_sync(0xffffffffu, n3);
-      const int4* slots = exchange(make_int4(n1, n2, n3, 0));
+      const uint32_t* words =
+          exchange(__reduce_add_sync(0xffffffffu, n1 | n2 << 10 | n3 << 20));
+      if (!words) return;
       n1 = n2 = n3 = 0;
       for (int w = lane; w < kWarps; w += 32) {
-        n1 += slots[w].x;
-        n2 += slots[w].y;
-        n3 += slots[w].z;
+        const uint32_t x = words[w];
+        n1 += x & 1023u;
+        n2 += (x >> 10) & 1023u;
+        n3 += x >> 20;
       }
       n1 = __reduce_add_sync(0xffffffffu, n1);
       n2 = __reduce_add_sync(0xffffffffu, n2);
@@ -373,15 +407,16 @@ __global__ void __cluster_dims__(kSelCluster, 1, 1) __launch_bounds__(THREADS, 1
   }
   sure &= open;
   at = exact ? 0u : at & open;
-  const int4* slots = exchange(make_int4(__reduce_add_sync(0xffffffffu, __popc(sure)),
-                                         __reduce_add_sync(0xffffffffu, __popc(at)), 0, 0));
+  const uint32_t* words =
+      exchange(__reduce_add_sync(0xffffffffu, __popc(sure) | __popc(at) << 16));
+  if (!words) return;
   int before_sure = 0, before_at = 0, all_sure = 0;
   for (int w = lane; w < kWarps; w += 32) {
-    const int4 v = slots[w];
-    all_sure += v.x;
+    const int x = words[w];
+    all_sure += x & 0xffff;
     if (w < warp) {
-      before_sure += v.x;
-      before_at += v.y;
+      before_sure += x & 0xffff;
+      before_at += x >> 16;
     }
   }
   all_sure = __reduce_add_sync(0xffffffffu, all_sure);
