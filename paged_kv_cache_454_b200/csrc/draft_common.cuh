@@ -61,6 +61,48 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
                : "memory");
 }
 
+// A page of one head (16 rows of D dims) moved by one copy, as rows of an operand
+// whose dims run along its 128-byte rows: 8-row groups kGroup bytes apart from page to
+// page, and for D = 128 the 64-dim halves of a group next to each other.  (Two copies
+// of 64 dims each, all 128 rows of a half together, hold a kernel that reads pages to
+// 5.6 TB/s: a copy costs its SM some 90 cycles, and the K of a decode step waited for
+// them, 84 against 77 us on 470 MB.)
+template <int D>
+struct KPage {
+  static constexpr int kBytes = 32 * D;
+  static constexpr int kGroup = 16 * D;
+  static constexpr int kHalf = 1024;
+  // of 16 dims i of a row
+  static __host__ __device__ constexpr uint32_t dims16(int i) {
+    return (i >> 2) * kHalf + (i & 3) * 32;
+  }
+  static bool encode(CUtensorMap* map, const void* pool, uint64_t rows) {
+    if (D == 128) {  // dims of a half, rows of a group, halves, groups
+      const uint64_t dims[4] = {64, 8, 2, rows / 8};
+      const uint64_t strides[3] = {D * 2, 128, D * 16};
+      const uint32_t box[4] = {64, 8, 2, 2};
+      return encode_bf16_map(map, pool, 4, dims, strides, box);
+    }
+    const uint64_t dims[2] = {D, rows};
+    const uint64_t strides[1] = {D * 2};
+    const uint32_t box[2] = {64, 16};
+    return encode_bf16_map(map, pool, 2, dims, strides, box);
+  }
+  // The page whose first pool row is `row`.
+  static __device__ __forceinline__ void load(uint32_t dst, const CUtensorMap* map, int row,
+                                              uint64_t* bar) {
+    if (D == 64) {
+      tc::tma_load_2d(dst, map, 0, row, bar);
+      return;
+    }
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%2, %2, %2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row >> 3), "r"(smem_u32(bar))
+        : "memory");
+  }
+};
+
 // Quotient of two non-negative numbers; a 64-bit division is ten times a 32-bit
 // one, and the numbers here rarely need it.
 __device__ __forceinline__ long long quotient(long long a, long long b) {

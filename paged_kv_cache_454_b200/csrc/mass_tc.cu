@@ -384,14 +384,13 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
         if (__any_sync(0xffffffffu, *abort_flag)) continue;
         if (lane == 0) {
           kmask[kt % kMaskRing] = vm;
-          mbar_arrive_expect_tx(&k_full[slot], __popc(vm) * C::kHalves * 2048);
+          mbar_arrive_expect_tx(&k_full[slot], __popc(vm) * KPage<D>::kBytes);
         }
         __syncwarp();
         if (get) {
           const int row = (pb * p.hkv + now.g) * 16;
-          const uint32_t dst = sbase + C::kOffK + slot * C::kTileBytes + lane * 2048;
-          tma_load_2d(dst, &p.tm_k, 0, row, &k_full[slot]);
-          if (D == 128) tma_load_2d(dst + kRegion, &p.tm_k, 64, row, &k_full[slot]);
+          KPage<D>::load(sbase + C::kOffK + slot * C::kTileBytes + lane * KPage<D>::kBytes, &p.tm_k,
+                         row, &k_full[slot]);
         }
         issued = kt + 1;
       }
@@ -442,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
     const uint32_t ubase = __shfl_sync(0xffffffffu, sbase, 0);
     const uint32_t utmem = __shfl_sync(0xffffffffu, tmem, 0);
     const uint64_t dq0 = smem_desc_sw128(ubase + C::kOffQ, 16, 1024);
-    const uint64_t dk0 = smem_desc_sw128(ubase + C::kOffK, 16, 1024);
+    const uint64_t dk0 = smem_desc_sw128(ubase + C::kOffK, 16, KPage<D>::kGroup);
     uint32_t qi = 0, kt0 = 0;
     uint32_t steps = 0;  // bit w: parity of warpgroup w's steps
     while (next_unit()) {
@@ -474,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
               const uint32_t off = (k >> 2) * kRegion + (k & 3) * 32;
-              umma_ss(utmem + 128 * w, desc_add(ka, off), desc_add(qb, off), idesc,
+              umma_ss(utmem + 128 * w, desc_add(ka, KPage<D>::dims16(k)), desc_add(qb, off), idesc,
                       k > 0 ? 1u : 0u);
             }
             umma_commit(&s_full[w]);
@@ -565,12 +564,7 @@ template <int D>
 int launch_mass(MassParams& p, const void* q, int64_t q_stride, const void* k_pool,
                 const pa_pool_desc& pool, int64_t most_tiles, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(pool.num_blocks) * pool.num_kv_heads * 16;
-  {
-    const uint64_t dims[2] = {static_cast<uint64_t>(D), static_cast<uint64_t>(rows)};
-    const uint64_t strides[1] = {D * 2};
-    const uint32_t box[2] = {64, 16};
-    if (!encode_bf16_map(&p.tm_k, k_pool, 2, dims, strides, box)) return PA_ERR_CUDA;
-  }
+  if (!KPage<D>::encode(&p.tm_k, k_pool, rows)) return PA_ERR_CUDA;
   {
     const uint64_t dims[3] = {static_cast<uint64_t>(D), static_cast<uint64_t>(p.hq),
                               static_cast<uint64_t>(p.total_q)};
