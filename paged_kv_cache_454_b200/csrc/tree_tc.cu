@@ -547,11 +547,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
 #pragma unroll
               for (int pg = 0; pg < 8; ++pg) {
                 if ((vm >> pg) & 1u) {
-                  if (v == 0) {  // K half by half, 128 rows each
-                    tma_load_2d(dst + pg * 2048, &p.tm_k, 0, y[pg], &kv_full[slot]);
-                    if (D == 128)
-                      tma_load_2d(dst + kRegion + pg * 2048, &p.tm_k, 64, y[pg], &kv_full[slot]);
-                  } else {  // V page by page, its halves next to each other
+                  if (v == 0) {
+                    KPage<D>::load(dst + pg * C::kPage, &p.tm_k, y[pg], &kv_full[slot]);
+                  } else {  // a page's 64-dim halves next to each other, 16 rows each
                     if (D == 128)
                       tma_load_3d(dst + pg * C::kPage, &p.tm_v, 0, y[pg], 0, &kv_full[slot]);
                     else
@@ -584,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
     const uint32_t ubase = __shfl_sync(0xffffffffu, sbase, 0);
     const uint32_t utmem = __shfl_sync(0xffffffffu, tmem, 0);
     const uint64_t dq0 = smem_desc_sw128(ubase + C::kOffQ, 16, 1024);
-    const uint64_t dk0 = smem_desc_sw128(ubase + C::kOffKV, 16, 1024);
+    const uint64_t dk0 = smem_desc_sw128(ubase + C::kOffKV, 16, KPage<D>::kGroup);
     const uint64_t dv0 = smem_desc_sw128(ubase + C::kOffKV, 2048, 1024);
     const uint32_t s_col = utmem + h * 128, o_col = utmem + kOCol + h * 128;
     uint32_t cnt = 0;   // this stream's tiles before the unit
@@ -611,12 +609,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
         mbar_wait(&pv_done[2 * h + half], ((cnt + (x >> 1)) & 1) ^ 1, abort_flag, p.err);
         if (__any_sync(0xffffffffu, *abort_flag)) return;
         tc_fence_after();
-        const uint64_t kb = desc_add(dk0, ks * C::kTileBytes + half * 8192);
+        const uint64_t kb = desc_add(dk0, ks * C::kTileBytes + half * 4 * C::kPage);
         if (elect_one()) {
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
             const uint32_t off = (i >> 2) * kRegion + (i & 3) * 32;
-            umma_ss(s_col + 64 * half, desc_add(qa, off), desc_add(kb, off), idesc_s,
+            umma_ss(s_col + 64 * half, desc_add(qa, off), desc_add(kb, KPage<D>::dims16(i)), idesc_s,
                     i > 0 ? 1u : 0u);
           }
           umma_commit(&s_full[2 * h + half]);
@@ -1052,7 +1050,7 @@ int launch_tree(TreeParams& p, const void* q, int64_t q_stride, const void* k_po
     const uint64_t dims[2] = {static_cast<uint64_t>(D), static_cast<uint64_t>(rows)};
     const uint64_t strides[1] = {D * 2};
     const uint32_t box[2] = {64, 16};
-    if (!encode_bf16_map(&p.tm_k, k_pool, 2, dims, strides, box)) return PA_ERR_CUDA;
+    if (!KPage<D>::encode(&p.tm_k, k_pool, rows)) return PA_ERR_CUDA;
     if (D == 64 && !encode_bf16_map(&p.tm_v, v_pool, 2, dims, strides, box)) return PA_ERR_CUDA;
   }
   if (D == 128) {
