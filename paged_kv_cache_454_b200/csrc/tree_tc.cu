@@ -740,7 +740,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
             // the context and in pages that were not loaded (their weights are 0,
             // and 0 times what is there could be NaN), and zero, on record, where
             // a drafted token's V is not finite (rows that do not see it have
-            // weight 0).
+            // weight 0).  Each row begins at a chunk of its own: at the same one,
+            // eight rows' would lie in the same banks.
             const int kr = r & 63, part = r >> 6;
             const int key = kv0 + kr;
             const uint32_t vpos = 2 * kt + 1;
@@ -752,16 +753,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
             bool odd = false;
             if (part < C::kHalves) {
               if (!dead && key >= c) {
-#pragma unroll 2
+#pragma unroll 4
                 for (int j = 0; j < 8; ++j) {
-                  const uint4 y = lds128(vrow + j * 16);
+                  const uint4 y = lds128(vrow + ((j + kr) & 7) * 16);
                   odd |= nonfinite_pair(y.x) | nonfinite_pair(y.y) | nonfinite_pair(y.z) |
                          nonfinite_pair(y.w);
                 }
               }
               if (dead || odd) {
-#pragma unroll 2
-                for (int j = 0; j < 8; ++j) sts128_zero(vrow + j * 16);
+#pragma unroll 4
+                for (int j = 0; j < 8; ++j) sts128_zero(vrow + ((j + kr) & 7) * 16);
                 fence_proxy_async_smem();
               }
             }
