@@ -34,7 +34,9 @@ namespace {
 constexpr int kRopeThreads = 256;
 constexpr int kRopeTokens = 4;  // tokens of a CTA
 constexpr int kRopeTokenThreads = kRopeThreads / kRopeTokens;
-constexpr int kRopeCtasPerSm = 2;  // fewer q CTAs than this: the q heads are split
+// Fewer q CTAs than this per SM: the q heads are split (two 28.3 | 3.8 us on 4288 and
+// 128 tokens, sixteen 30.3 | 4.2).
+constexpr int kRopeCtasPerSm = 2;
 constexpr int kRopeRows = 3;       // rows of a lane group in flight
 
 struct RopeParams {

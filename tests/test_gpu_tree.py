@@ -310,3 +310,56 @@ def test_bad_block_in_the_middle_of_two_row_tiles():
                 assert abs(float(lse[r0 + i, h]) - e) <= 2e-5 + 1e-6 * abs(e)
                 d = np.abs(H.host_f64(out[r0 + i, h]) - o)
                 assert np.all(d <= 2.0 ** -8 * np.abs(o) + 3e-4)
+
+
+@pytest.mark.parametrize("n,hq,hkv,d", [(3, 4, 4, 128), (20, 16, 2, 64), (40, 16, 2, 128)])
+def test_contexts_that_end_in_either_half_of_a_tile(n, hq, hkv, d):
+    # the drafted tokens cross the halves of a tile, or the last half holds no key
+    rng = np.random.default_rng(n)
+    for ends in ([1, 63, 64, 65, 127, 128], [64] * 6, [1, 128] * 3, [20, 70, 64, 65, 33, 1]):
+        lens = [128 * int(rng.integers(0, 5)) + e for e in ends * 2]
+        lens = [L if L >= n else L + 128 for L in lens]
+        b = Batch(sum(lens) + n, lens, [n] * len(lens), hq, hkv, d)
+        out, lse = pa().pa_tree_attention(**b.device(), want_lse=True)
+        check(out, lse, b.want())
+    # one long item shared by all CTAs
+    for L in (128 * 80 + 2, 128 * 80 + 64, 128 * 81):
+        b = Batch(L, [L], [n], hq, hkv, d)
+        out, lse = pa().pa_tree_attention(**b.device(), want_lse=True)
+        check(out, lse, b.want())
+    assert pa().pa_get_device_error() == 0
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(64, 8, 128), (32, 32, 128), (32, 8, 64)])
+def test_results_are_the_same_every_time(hq, hkv, d):
+    # items of one and of two row tiles, short and long ones, in turn on the same CTAs:
+    # each stream of a CTA passes over what is the other's, and equal inputs give equal
+    # bits however the copies arrive; two batches between which nothing waits
+    import torch
+    states = []
+    for seed in (1, 2):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        rng = np.random.default_rng(seed)
+        n = rng.integers(7, 64, 40)
+        lens = np.maximum(n + 1, np.exp(rng.uniform(np.log(130), np.log(9000), 40)).astype(int))
+        blocks = -(-lens // 16)
+        nb = int(blocks.sum())
+        tables = np.zeros((40, int(blocks.max())), np.int32)
+        order, at = rng.permutation(nb), 0
+        for s, k in enumerate(blocks):
+            tables[s, :k] = order[at:at + k]
+            at += k
+        rand = lambda *shape: torch.randn(shape, generator=g, device="cuda", dtype=torch.bfloat16)
+        total = int(n.sum())
+        mask = torch.randint(-2 ** 63, 2 ** 63 - 1, (total, 1), generator=g, device="cuda")
+        states.append(dict(q=rand(total, hq, d), max_q_len=64, tree_mask=mask,
+                           cu_q_lens=H.dev_i32(np.concatenate([[0], np.cumsum(n)])),
+                           k_pool=rand(nb, hkv, 16, d), v_pool=rand(nb, hkv, 16, d),
+                           block_tables=H.dev_i32(tables), context_lens=H.dev_i32(lens),
+                           scale=d ** -0.5))
+    first = [pa().pa_tree_attention(**s, want_lse=True) for s in states]
+    for _ in range(60):
+        got = [pa().pa_tree_attention(**s, want_lse=True) for s in states]
+        for (o, e), (o0, e0) in zip(got, first):
+            assert torch.equal(o, o0) and torch.equal(e, e0)
+    assert pa().pa_get_device_error() == 0
