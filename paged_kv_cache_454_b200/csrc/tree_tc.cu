@@ -22,8 +22,8 @@
 // works on one half, the other's weights are multiplied and the half after that
 // is scored (with one buffer of a whole tile, scores, softmax and product follow
 // each other and the tensor cores idle half the time: 533 against 404 us on 48
-// sequences).  The ring of K and V holds whole tiles: slots of half a tile, freed
-// earlier, measured 94 against 91 us on 24 sequences of 32/32 heads.  A thread takes its 64 scores into registers once and puts the
+// sequences).  K and V have five slots of a tile at D = 128 (four: 111 against 96
+// us on 24 sequences of 32/32 heads, 480 against 407 on 48 of 64/8).  A thread takes its 64 scores into registers once and puts the
 // weights back once: tensor memory answers between products, so every round trip
 // to it waits.
 //
