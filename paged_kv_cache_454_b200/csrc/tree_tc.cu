@@ -279,7 +279,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
   uint64_t* s_full = u_empty + kUnits;  // [stream][half]: scores ready
   uint64_t* p_full = s_full + 4;        // weights written back
   uint64_t* pv_done = p_full + 4;       // P.V complete
-  uint64_t* o_free = pv_done + 4;       // both accumulators of a unit read out
+  uint64_t* o_free = pv_done + 4;       // both accumulators of a unit read out, and
+                                        // both MMA warps past the unit's wait for it
   uint64_t* drain = o_free + 1;         // per stream
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
@@ -321,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
     }
     mbar_init(&drain[0], 1);
     mbar_init(&drain[1], 1);
-    mbar_init(o_free, 8);
+    mbar_init(o_free, 8 + 2);  // softmax warps, and the MMA warps past their wait
     *abort_flag = 0;
     prefetch_tmap(&p.tm_k);
     prefetch_tmap(&p.tm_v);
@@ -656,8 +657,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
         scores(0);
         scores(1);
       }
-      // (every unit's, so its parity is never taken for another's)
+      // Every unit's, and the next phase ends only when both MMA warps have passed this
+      // wait: a stream without a tile in a unit is not waited for otherwise, and one that
+      // came a unit late would take the parity of the phase it waits for for that of the
+      // next and wait for a unit that needs it.
       mbar_wait(o_free, (unit & 1) ^ 1, abort_flag, p.err);
+      if (lane == 0) mbar_arrive(o_free);
       for (int x = 0; x < 2 * tiles; ++x) {
         const int half = x & 1;
         const uint32_t vpos = position(x) + 1;

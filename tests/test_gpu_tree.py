@@ -363,3 +363,23 @@ def test_results_are_the_same_every_time(hq, hkv, d):
         for (o, e), (o0, e0) in zip(got, first):
             assert torch.equal(o, o0) and torch.equal(e, e0)
     assert pa().pa_get_device_error() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_runs_of_one_tile_units_between_pairs(d):
+    # a dozen units of one key tile on every CTA, in which one of the two streams has
+    # nothing to do, with items of two row tiles among them
+    rng = np.random.default_rng(d)
+    n = rng.choice([1, 4, 16, 20, 31], 220)
+    lens = np.minimum(128, n + rng.integers(0, 128, 220))
+    b = Batch(71 + d, lens, n, 64, 8, d)
+    dev = b.device()
+    first = pa().pa_tree_attention(**dev, want_lse=True)
+    for _ in range(30):
+        out, lse = pa().pa_tree_attention(**dev, want_lse=True)
+        assert bool((out == first[0]).all()) and bool((lse == first[1]).all())
+    assert pa().pa_get_device_error() == 0
+    rows = int(b.cu[30])  # of the first thirty sequences
+    want = drafting.tree_attention(b.h["q"][:rows], b.cu[:31], b.mask[:rows], b.kp, b.vp,
+                                   b.lay.block_tables[:30], b.lay.context_lens[:30], b.lay.scale)
+    check(*first, want, rows=np.arange(rows))
