@@ -102,6 +102,17 @@ __device__ __forceinline__ int block_scan(int x, int* warp_tot) {
   return r;
 }
 
+// The plan is a programmatic dependent of the kernel before it (the cache write that
+// puts this step's tokens in the pool, a prefill, any attention): it reads the tables
+// and lengths and searches them while that kernel finishes.  Its workspace may be that
+// kernel's own scratch, or memory that was its input until a moment ago, so a thread
+// waits for that kernel's end before its first global write (the second time the wait
+// is over at once).  The decode kernel, which waits for this grid, then sees the pool
+// as written.
+__device__ __forceinline__ void wait_before_writes() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 __global__ void __launch_bounds__(1024) decode_plan_kernel(const int32_t* __restrict__ context_lens,
                                                            const int32_t* __restrict__ block_tables,
                                                            int S, int max_blocks, int hkv,
@@ -360,6 +371,7 @@ __global__ void __launch_bounds__(1024) decode_plan_kernel(const int32_t* __rest
             open = false;
           }
         }
+        wait_before_writes();
         if (live) {
           const int span = lcp * 16 >= kMinCascSpan ? lcp * 16 : 0;
           int* rr = runs + static_cast<int64_t>(r) * kRunInts;
@@ -402,6 +414,7 @@ __global__ void __launch_bounds__(1024) decode_plan_kernel(const int32_t* __rest
   }
 
   // ---- partitions per sequence and their exclusive prefix ----
+  wait_before_writes();
   if (tid == 0) carry = 0;
   if (tid < kMaxBuckets) bucket[tid] = 0;
   __syncthreads();
@@ -567,19 +580,13 @@ __global__ void __launch_bounds__(1024) decode_plan_kernel(const int32_t* __rest
     }
   }
   for (int i = tid; i < S * kv_heads; i += 1024) merge_cnt[i] = 0;
-  // The plan is a programmatic dependent of the kernel before it (the cache
-  // write that puts this step's tokens in the pool, or a prefill): it reads
-  // only the tables and lengths, so it runs while that kernel finishes, and
-  // it completes only after that kernel has -- the decode kernel, which waits
-  // for this grid, then sees the pool as written.
-  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 }  // namespace
 
 int launch_decode_plan(const DecodeArgs& a) {
-  // a programmatic dependent of the previous kernel on the stream (see the end
-  // of the kernel)
+  // a programmatic dependent of the previous kernel on the stream (see
+  // wait_before_writes)
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(1);
   cfg.blockDim = dim3(1024);

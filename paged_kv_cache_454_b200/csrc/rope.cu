@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_cons
   constexpr int kGroups = kRopeTokenThreads / kLanes;  // rows of a token in work at once
   __shared__ float2 turn[kRopeTokens][D / 2];
   // a decode plan launched after this kernel may start now (it reads only the
-  // tables and lengths, and waits for this grid before it completes)
+  // tables and lengths before this grid has ended, and writes nothing)
   if (kCache) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int mine = threadIdx.x / kRopeTokenThreads;  // which of the CTA's tokens
   const int at = threadIdx.x % kRopeTokenThreads;
