@@ -51,8 +51,8 @@ extern "C" {
  * mass_stride) is left out and sets PA_DEV_ERR_CONTEXT.  The tokens of a bad
  * block id add nothing (mass_out = mass_in) and set PA_DEV_ERR_BLOCK_ID.
  * A sum runs over the rows in a fixed order: equal inputs give equal bits.
- * Stream order: as with pa_tree_attention (cu_q_lens and context_lens must be final
- * before a kernel that signals early; everything else is read after it).
+ * Stream order: as with pa_tree_attention (nothing is read or written before the
+ * kernel before has finished).
  */
 #define PA_MASS_MAX_QUERIES (1 << 20)
 

@@ -60,11 +60,9 @@ extern "C" {
  * token whose V holds one makes the outputs of the rows that see it NaN (all
  * head_dim values) and leaves the other rows as they are.
  *
- * Stream order: as with pa_decode, the call's first kernel may be set up while the
- * kernel before it on `stream` ends.  If that kernel signals that its dependents may
- * start early (this library's cache writes and attention kernels do), cu_q_lens and
- * context_lens are read while it still runs -- they must be final by then; nothing
- * else is read before it has finished.
+ * Stream order: the call's first kernel may be set up while the kernel before it on
+ * `stream` ends, but reads and writes nothing before it has finished: any argument may
+ * be the result of the kernel directly before, and the workspace its scratch.
  *
  * Precision: scores and the P.V product accumulate in fp32, the running maximum
  * and sum are fp32, and the softmax weights enter P.V as a bf16 part and the bf16

@@ -7,7 +7,7 @@
 namespace pa {
 
 // (Not the read-only path: what is read here may have been written by a kernel that
-// still ran when this one was set up.)
+// still ran when this one was set up, before griddepcontrol.wait.)
 __device__ __forceinline__ int ld_i32(const int32_t* ptr) {
   int x;
   asm volatile("ld.global.b32 %0, [%1];" : "=r"(x) : "l"(ptr));
@@ -133,8 +133,9 @@ __device__ __forceinline__ long long cta_scan(long long mine, long long* slots, 
   return before;
 }
 
-// Launch of a kernel that may be set up while the one before it on the stream ends
-// (it waits for that one's end itself, before it reads anything).
+// Launch of a kernel that may be set up while the one before it on the stream ends.
+// Before its griddepcontrol.wait it may only prepare its own shared and tensor memory:
+// it reads no global memory (the lengths included) and writes none.
 template <typename P>
 inline int launch_overlapped(void (*kernel)(P), dim3 grid, int threads, int smem, const P& p,
                              cudaStream_t stream) {

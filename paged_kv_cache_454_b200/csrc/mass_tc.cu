@@ -211,10 +211,11 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
     prefetch_tmap(&p.tm_k);
     prefetch_tmap(&p.tm_q);
   }
-  // This kernel may have been set up while the one before it ran, and reads nothing
-  // but the lengths before that one's end.
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp == 1) tmem_alloc(tmem_slot, kTmemCols);
+  // As in the tree kernel: nothing is read before the kernel before has ended, and the
+  // one after may be set up only from then on.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // Where this CTA's stretch begins: as in the tree kernel, a scan over the
   // threads' runs of sequences.
@@ -258,7 +259,6 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
   }
   fence_barrier_init();
   tc_fence_before();
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;

@@ -328,11 +328,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
     prefetch_tmap(&p.tm_v);
     prefetch_tmap(&p.tm_q);
   }
-  // The merge kernel may be set up now (it waits for this grid's end); this one may
-  // have been while the kernel before it ran, and reads nothing but the lengths
-  // before that one's end.
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp == 1) tmem_alloc(tmem_slot, kTmemCols);
+  // This kernel may have been set up while the one before it ran; it reads nothing
+  // before that one's end, the lengths among it (without the wait their last write need
+  // not be visible, and CTAs that read different ones would not agree on the line).  The
+  // merge kernel may be set up now, not sooner: whatever starts early overlaps one
+  // kernel only, the one before it.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // Where this CTA's stretch begins.  Thread i sums a run of sequences, a scan
   // over the threads places the runs on the line, and the thread whose run holds
@@ -381,7 +384,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
   }
   fence_barrier_init();
   tc_fence_before();
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
@@ -1018,8 +1020,8 @@ constexpr int kMergeWarps = 4;
 template <int D>
 __global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(
     const __grid_constant__ TreeParams p) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int4 b = p.border[blockIdx.x];
   if (b.x < 0) return;
   const int lane = threadIdx.x & 31;

@@ -155,3 +155,47 @@ def test_inputs_of_a_cache_write_become_the_workspace():
         return res + [st.k.clone(), st.v.clone()]
 
     runs(order, 60)
+
+
+def test_lengths_written_by_the_kernel_before():
+    # directly before tree attention, weight and decode: by an elementwise kernel and by
+    # an eviction
+    st = Step(2, 5)
+    full = st.lens.clone()
+    short = full - 100
+    cu = st.cu.clone()
+    budgets = H.dev_i32([200] * S)
+
+    def order(sync):
+        st.mass.copy_(st.mass0)
+        st.k.copy_(st.k0)
+        st.v.copy_(st.v0)
+        res = []
+        for lens in (short, full):
+            st.lens.copy_(lens)
+            res += st.tree()
+            sync()
+            st.cu.zero_()
+            sync()
+            st.lens.add_(-3)
+            st.cu.add_(cu)
+            res += st.tree()
+            sync()
+            out, lse = st.decode()
+            st.lens.sub_(0)
+            res += [out, lse, st.weigh(lse).clone()]
+            sync()
+        keep = st.lens
+        _, st.lens, _ = pa().pa_evict(st.mass, st.k, st.v, st.tables, st.lens, budgets, sink=2,
+                                      recent=N)
+        sync()
+        res += st.tree()
+        sync()
+        res += st.decode()
+        sync()
+        res.append(st.lens)
+        st.lens = keep
+        return res
+
+    st.mass0, st.k0, st.v0 = st.mass + 1, st.k.clone(), st.v.clone()
+    runs(order, 40)
