@@ -65,8 +65,10 @@ extern "C" {
  * be the result of the kernel directly before, and the workspace its scratch.
  *
  * Precision: scores and the P.V product accumulate in fp32, the running maximum
- * and sum are fp32, and the softmax weights enter P.V as a bf16 part and the bf16
- * part of what that leaves (within 2^-15 of the weight); out is rounded once.
+ * and sum are fp32, and the softmax weights enter P.V as their nearest bf16 and the
+ * nearest bf16 of what that leaves (within 2^-17 of the weight); out is rounded once.
+ * Weights reach 2^16 before the division by their sum, so |V| has to stay below 2^90
+ * (with up to 2^20 keys) for the sums to stay finite.
  */
 PA_API size_t pa_tree_workspace_size(int32_t max_q_len, int32_t num_q_heads, pa_pool_desc pool);
 

@@ -7,8 +7,8 @@
 // of 128, half a tile (64 keys) per step:
 //     S [128 x 64] = Q . K^T             (D/16 MMAs)
 //     O [128 x D] += P . V               (4 MMAs of P_hi, 4 of P_lo)
-// with fp32 accumulators in tensor memory; P = P_hi + P_lo, the weight with its
-// mantissa cut to bf16 and the same cut of the rest, replaces its scores in
+// with fp32 accumulators in tensor memory; P = P_hi + P_lo, the weight rounded to
+// bf16 and what that leaves rounded likewise, replaces its scores in
 // tensor memory (per 16 keys: 8 columns of P_hi, 8 of P_lo) and is read there by
 // the second product.
 //
@@ -862,7 +862,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
             }
           }
           // Weights, in place of the scores: per 16 keys 8 columns of P_hi and 8 of
-          // P_lo.
+          // P_lo.  Both parts are rounded to nearest (cut off instead, which takes as
+          // long, they made every output smaller by some 2^-17 of itself: l sums the
+          // whole weights).
           const float nm = m == -CUDART_INF_F ? 0.f : -m;
           const float2 nm2 = make_float2(nm, nm);
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -875,12 +877,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
                   __ffma2_rn(make_float2(s[16 * j + i], s[16 * j + i + 1]), sc2, nm2);
               const float2 e = make_float2(exp2f(y.x), exp2f(y.y));
               sum[(i >> 1) & 1] = __fadd2_rn(sum[(i >> 1) & 1], e);
-              const uint32_t ex = __float_as_uint(e.x), ey = __float_as_uint(e.y);
-              w[i >> 1] = __byte_perm(ex, ey, 0x7632);
-              const float2 hi = make_float2(__uint_as_float(ex & 0xffff0000u),
-                                            __uint_as_float(ey & 0xffff0000u));
+              const uint32_t h2 = pack_bf16x2(e.x, e.y);
+              w[i >> 1] = h2;
+              const float2 hi = make_float2(bf16lo(h2), bf16hi(h2));
               const float2 lo = __ffma2_rn(hi, neg1, e);  // e - P_hi, exact
-              w[8 + (i >> 1)] = __byte_perm(__float_as_uint(lo.x), __float_as_uint(lo.y), 0x7632);
+              w[8 + (i >> 1)] = pack_bf16x2(lo.x, lo.y);
             }
             tmem_st16_nowait(scol + 16 * j, w);
           }

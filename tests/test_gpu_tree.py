@@ -383,3 +383,32 @@ def test_runs_of_one_tile_units_between_pairs(d):
     want = drafting.tree_attention(b.h["q"][:rows], b.cu[:31], b.mask[:rows], b.kp, b.vp,
                                    b.lay.block_tables[:30], b.lay.context_lens[:30], b.lay.scale)
     check(*first, want, rows=np.arange(rows))
+
+
+def test_outputs_are_rounded_both_ways_alike():
+    # Outputs that differ from the 64-bit result rounded to bf16 lie one step above or
+    # below it, by chance: of m of them, those towards zero exceed the others by 5 sqrt(m)
+    # at most, and by what a systematic loss turns: the accumulator is cut off, by 2^-24
+    # of itself on average, after each of 32 products (200 keys, 16 a time, two parts of
+    # the weight), and a loss of 2^-19 crosses a border between steps of 2^-8 or more for
+    # 2^-11 of the outputs at most.
+    import torch
+    s, n, hq, hkv, d, L = 16, 16, 64, 8, 128, 200
+    g = torch.Generator(device="cuda").manual_seed(3)
+    rand = lambda *shape: torch.randn(shape, generator=g, device="cuda",  # noqa: E731
+                                      dtype=torch.bfloat16)
+    blocks = -(-L // 16)
+    q, k, v = rand(s * n, hq, d), rand(s * blocks, hkv, 16, d), rand(s * blocks, hkv, 16, d)
+    tables = torch.randperm(s * blocks, generator=g, device="cuda").int().view(s, blocks)
+    out, _ = pa().pa_tree_attention(q, H.dev_i32(n * np.arange(s + 1)), n,
+                                    torch.full((s * n, 1), -1, device="cuda"), k, v, tables,
+                                    H.dev_i32([L] * s), d ** -0.5)
+    rows = lambda pool: pool[tables.long()].transpose(2, 3).reshape(  # noqa: E731
+        s, 16 * blocks, hkv, d)[:, :L].double()
+    x = torch.einsum("sihgd,sthd->sihgt", q.double().view(s, n, hkv, hq // hkv, d), rows(k))
+    p = torch.softmax(x * float(np.float32(d ** -0.5)), -1)
+    want = torch.einsum("sihgt,sthd->sihgd", p, rows(v)).reshape(s * n, hq, d)
+    nearest = want.to(torch.bfloat16)
+    off = (out.double() - nearest.double()) * want.sign()
+    low, high = int((off < 0).sum()), int((off > 0).sum())
+    assert abs(low - high) <= 5 * (low + high) ** 0.5 + 2.0 ** -11 * want.numel(), (low, high)
