@@ -35,9 +35,16 @@ extern "C" {
  *
  *   q            bf16 [total_q][num_q_heads][head_dim], token stride q_stride;
  *                total_q >= 1.
- *   lse          float [total_q][num_q_heads]: what pa_decode, pa_chunked_prefill
- *                or pa_tree_attention returned for these rows (-inf: the row
- *                adds nothing).
+ *   lse          float [total_q][num_q_heads]: the log-sum-exp of these rows over
+ *                the keys they see here, as pa_decode and pa_chunked_prefill return
+ *                it (an infinite one: the row adds nothing, whatever its scores are).
+ *                pa_tree_attention's is that of a row whose mask is the chain of its
+ *                own and all earlier tokens.  The row of a token on a branch has not
+ *                seen the other branches, whose weights here would have no bound: pass
+ *                the accepted branch instead, after pa_compact_tokens has packed it
+ *                behind the cache -- its rows of q and lse in order, n its tokens,
+ *                context_lens the cached ones and those -- where each row sees just
+ *                what it saw in the tree.
  *   cu_q_lens    int32 [num_seqs + 1], device; or NULL: a decode step, row s is
  *                sequence s's only query (total_q = num_seqs, max_q_len = 1).
  *   max_q_len    host bound on any n (larger ones are left out); at most

@@ -547,8 +547,10 @@ def pa_attention_mass(q, lse, cu_q_lens, max_q_len, k_pool, block_tables, contex
                       mass_in=None, mass=None, stream=None):
     """Add to every cached token the softmax weights that the rows of ``q`` (bf16
     [total_q, Hq, D], with the ``lse`` fp32 [total_q, Hq] their attention returned)
-    gave it.  ``cu_q_lens`` int32 [S+1] on the device, or None for a decode step
-    (one row per sequence).  ``mass_in``: fp32 [S, Hkv, W] so far (None: zeros);
+    gave it.  Query i of a sequence's n sees all but the last n - 1 - i tokens: of a
+    tree only the accepted branch, packed by ``pa_compact_tokens``, is such a chain.
+    ``cu_q_lens`` int32 [S+1] on the device, or None for a decode step (one row per
+    sequence).  ``mass_in``: fp32 [S, Hkv, W] so far (None: zeros);
     ``mass``: where the sums go (may be ``mass_in``; default: a new tensor, zero
     past each sequence's length).  Returns ``mass``."""
     torch = _torch()

@@ -29,6 +29,8 @@
 // four warpgroups.  Every wait is bounded.
 #include <math_constants.h>
 
+#include <type_traits>
+
 #include "../../include/pa_evict.h"
 #include "draft_common.cuh"
 #include "internal.h"
@@ -516,24 +518,39 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
         const float* e = lse_s + (qi % kQSlots) * 128;
         mbar_wait(&s_full[wg], steps & 1, abort_flag, p.err);
         tc_fence_after();
+        auto add_columns = [&](auto careful_v) {
+          constexpr bool careful = decltype(careful_v)::value;
 #pragma unroll 1
-        for (int c0 = 0; c0 < cols; c0 += 16) {
-          float x[16];
-          tmem_ld16(scol + c0, x);
+          for (int c0 = 0; c0 < cols; c0 += 16) {
+            float x[16];
+            tmem_ld16(scol + c0, x);
 #pragma unroll
-          for (int c = 0; c < 16; c += 4) {
-            const float4 l4 = *reinterpret_cast<const float4*>(e + c0 + c);
-            const float l[4] = {l4.x, l4.y, l4.z, l4.w};
+            for (int c = 0; c < 16; c += 4) {
+              const float4 l4 = *reinterpret_cast<const float4*>(e + c0 + c);
+              const float l[4] = {l4.x, l4.y, l4.z, l4.w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int col = c0 + c + k;
-              const float y = col >= from && col < cols ? fmaf(x[c + k], sc, -l[k]) : -CUDART_INF_F;
-              if (k & 1)
-                sum1 += exp2f(y);
-              else
-                sum0 += exp2f(y);
+              for (int k = 0; k < 4; ++k) {
+                const int col = c0 + c + k;
+                const bool add = col >= from && col < cols && !(careful && l[k] == CUDART_INF_F);
+                const float y = add ? fmaf(x[c + k], sc, -l[k]) : -CUDART_INF_F;
+                if (k & 1)
+                  sum1 += exp2f(y);
+                else
+                  sum0 += exp2f(y);
+              }
             }
           }
+        };
+        const float had0 = sum0, had1 = sum1;
+        add_columns(std::false_type{});
+        // A row that saw nothing (its l is infinite) adds nothing, whatever it scores: an
+        // infinite score or a NaN left the sum infinite or NaN, and the columns are gone
+        // through once more, without such rows.  (A comparison per score instead: 20.2
+        // against 19.1 us on 9 sequences of 500 to 4203 tokens with 17 to 40 queries.)
+        if (__any_sync(0xffffffffu, !(sum0 + sum1 < CUDART_INF_F))) {
+          sum0 = had0;
+          sum1 = had1;
+          add_columns(std::true_type{});
         }
         tc_fence_before();
         __syncwarp();

@@ -240,3 +240,70 @@ def test_bad_blocks_among_sequences_without_rows():
             got = pa().pa_attention_mass(**dev)
             b.check(got, want=want)
         assert pa().pa_get_device_error() == pa().PA_DEV_ERR_BLOCK_ID
+
+
+def test_a_row_that_saw_nothing_adds_nothing_whatever_it_scores():
+    # lse -inf, and keys whose scores are infinite or NaN: one that only such a row sees,
+    # and a whole sequence of such rows
+    b = Batch(45, [90, 200, 64], [4, 3, 1], 8, 2, 64)
+    b.lse[3] = -np.inf          # the last row of sequence 0
+    b.lse[4:7] = -np.inf        # all of sequence 1
+    kp = b.kp.copy()
+
+    def fill(s, t, bits):
+        kp[int(b.lay.block_tables[s, t // 16]), :, t % 16] = bits
+
+    fill(0, 89, 0x7F80)         # +inf (times q of either sign)
+    fill(1, 0, 0x7FC0)          # NaN
+    fill(1, 77, 0x7F80)
+    fill(1, 199, 0xFF80)
+    dev = b.device()
+    dev["k_pool"] = H.dev_bf16(kp)
+    want = [np.array(w) for w in b.want()]
+    got = pa().pa_attention_mass(**dev)
+    assert bool((got[1] == 0).all()) and bool((got[0, :, 89] == 0).all())
+    b.check(got, want=want)
+    assert pa().pa_get_device_error() == 0
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(16, 2, 128), (4, 4, 64)])
+def test_weights_of_an_accepted_branch(hq, hkv, d):
+    # A tree whose rejected siblings score high: after packing, the accepted rows are a
+    # chain, and their weights (with the lse the tree gave) sum to 1 a row and head.
+    c = [130, 47]
+    parent = [-1, 0, 0, 1, 2, 4, 4]
+    branch = [0, 2, 4, 6]
+    n, m = len(parent), len(branch)
+    bits = []
+    for i, p in enumerate(parent):
+        bits.append((1 << i) | (bits[p] if p >= 0 else 0))
+    b = Batch(47, [x + n for x in c], [n, n], hq, hkv, d)
+    kp = b.kp.copy()
+    for s, x in enumerate(c):
+        for i in set(range(n)) - set(branch):  # aligned with every query of the group
+            t = x + i
+            for g in range(hkv):
+                k = 8 * oracle.bf16_bits_to_f64(b.h["q"][s * n + 6, g * (hq // hkv)])
+                kp[int(b.lay.block_tables[s, t // 16]), g, t % 16] = synth.f32_to_bf16_bits(
+                    k.astype(np.float32))
+    dk, dv = H.dev_bf16(kp), H.dev_bf16(b.vp)
+    tables, scale = H.dev_i32(b.lay.block_tables), b.lay.scale
+    q = H.dev_bf16(b.h["q"])
+    _, lse = pa().pa_tree_attention(q, H.dev_i32(b.cu), n, H.dev_i64(np.array(bits * 2)[:, None]),
+                                    dk, dv, tables, H.dev_i32([x + n for x in c]), scale,
+                                    want_lse=True)
+    pa().pa_compact_tokens(dk, dv, tables, H.dev_i32([[branch], [branch]]), H.dev_i32([m, m]),
+                           base=H.dev_i32(c))
+    import torch
+    rows = torch.tensor([s * n + i for s in range(2) for i in branch], device="cuda")
+    lens = [x + m for x in c]
+    mass = pa().pa_attention_mass(q[rows], lse[rows], H.dev_i32([0, m, 2 * m]), m, dk, tables,
+                                  H.dev_i32(lens), scale)
+    want = drafting.attention_mass(b.h["q"][rows.cpu().numpy()], lse[rows].cpu().numpy(),
+                                   [0, m, 2 * m], H.host_bits(dk), b.lay.block_tables,
+                                   np.array(lens), scale)
+    b.lens = np.array(lens)
+    b.check(mass, want=want)
+    # a row's weights sum to 1: each is off by its score's error and the lse's, 8e-5 together
+    assert float((mass.sum(2) - m * (hq // hkv)).abs().max()) <= 1e-4 * m * (hq // hkv)
+    assert pa().pa_get_device_error() == 0
