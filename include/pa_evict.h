@@ -49,7 +49,8 @@ extern "C" {
  *                sequence s's only query (total_q = num_seqs, max_q_len = 1).
  *   max_q_len    host bound on any n (larger ones are left out); at most
  *                PA_MASS_MAX_QUERIES.
- *   mass_in      the weights so far, or NULL for none.
+ *   mass_in      the weights so far, of every t < context_len (a token that this
+ *                step wrote: 0, or see pa_attention_mass_ex), or NULL for none.
  *   mass_out     may be mass_in.  Entries at and past a sequence's length are
  *                not written.
  *   mass_stride  floats between two heads of both, >= every context length.
@@ -70,6 +71,24 @@ PA_API int pa_attention_mass(const void* q, int64_t q_stride, const float* lse,
                              int32_t num_seqs, int32_t num_q_heads, float scale,
                              const float* mass_in, float* mass_out, int64_t mass_stride,
                              void* stream);
+
+/*
+ * pa_attention_mass_ex -- pa_attention_mass with flags (0: as above).
+ *   PA_MASS_OWN_FROM_ZERO  a step's own tokens (t >= c) had no weight before it:
+ *     mass_in is read for t < c only.  Without it mass_in[t] of a token written this
+ *     step has to be 0, which it is not behind an eviction that packed the weights in
+ *     place, nor where a rejected draft's token lay.
+ */
+#define PA_MASS_OWN_FROM_ZERO 0x1
+
+PA_API int pa_attention_mass_ex(const void* q, int64_t q_stride, const float* lse,
+                                const int32_t* cu_q_lens, int32_t total_q, int32_t max_q_len,
+                                const void* k_pool, pa_pool_desc pool,
+                                const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                const int32_t* context_lens, int32_t num_seqs,
+                                int32_t num_q_heads, float scale, const float* mass_in,
+                                float* mass_out, int64_t mass_stride, uint32_t flags,
+                                void* stream);
 
 /*
  * pa_evict -- bring every sequence down to its budget.  Of L = context_lens[s]
@@ -93,7 +112,8 @@ PA_API int pa_attention_mass(const void* q, int64_t q_stride, const float* lse,
  *                tokens' weights, packed alike (-0 becomes 0, a NaN the canonical
  *                one).  May be mass with the same stride.
  * Entries of kept and mass_out past keep, rows of the cache past it, and blocks
- * of the table that are no longer needed are left as they were.  A length
+ * of the table that are no longer needed are left as they were (so the tokens written
+ * there next have no weight of their own yet: see PA_MASS_OWN_FROM_ZERO).  A length
  * outside [0, max_blocks_per_seq * block_size] or beyond mass_stride counts as 0
  * and sets PA_DEV_ERR_CONTEXT; a bad block id leaves its rows unmoved and sets
  * PA_DEV_ERR_BLOCK_ID.

@@ -544,7 +544,7 @@ def pa_tree_attention(q, cu_q_lens, max_q_len, tree_mask, k_pool, v_pool, block_
 
 
 def pa_attention_mass(q, lse, cu_q_lens, max_q_len, k_pool, block_tables, context_lens, scale,
-                      mass_in=None, mass=None, stream=None):
+                      mass_in=None, mass=None, stream=None, own_from_zero=False):
     """Add to every cached token the softmax weights that the rows of ``q`` (bf16
     [total_q, Hq, D], with the ``lse`` fp32 [total_q, Hq] their attention returned)
     gave it.  Query i of a sequence's n sees all but the last n - 1 - i tokens: of a
@@ -552,7 +552,9 @@ def pa_attention_mass(q, lse, cu_q_lens, max_q_len, k_pool, block_tables, contex
     ``cu_q_lens`` int32 [S+1] on the device, or None for a decode step (one row per
     sequence).  ``mass_in``: fp32 [S, Hkv, W] so far (None: zeros);
     ``mass``: where the sums go (may be ``mass_in``; default: a new tensor, zero
-    past each sequence's length).  Returns ``mass``."""
+    past each sequence's length).  ``own_from_zero``: the tokens of this step start
+    from 0 whatever ``mass_in`` holds for them (what an eviction in place or a rejected
+    draft left); without it ``mass_in`` has to be 0 there.  Returns ``mass``."""
     torch = _torch()
     dev = q.device
     f32 = torch.float32
@@ -580,9 +582,10 @@ def pa_attention_mass(q, lse, cu_q_lens, max_q_len, k_pool, block_tables, contex
     if mass.shape != (seqs, desc.num_kv_heads, width) or (
             mass_in is not None and mass_in.shape != mass.shape):
         raise ValueError(f"mass and mass_in must be [{seqs}, {desc.num_kv_heads}, W] alike")
-    _run("pa_attention_mass", dev, stream, q.data_ptr(), qs, lse.data_ptr(), _ptr(cu_q_lens),
+    _run("pa_attention_mass_ex", dev, stream, q.data_ptr(), qs, lse.data_ptr(), _ptr(cu_q_lens),
          total_q, int(max_q_len), k_pool.data_ptr(), desc, block_tables.data_ptr(), blocks,
-         context_lens.data_ptr(), seqs, hq, float(scale), _ptr(mass_in), mass.data_ptr(), width)
+         context_lens.data_ptr(), seqs, hq, float(scale), _ptr(mass_in), mass.data_ptr(), width,
+         _abi.PA_MASS_OWN_FROM_ZERO if own_from_zero else 0)
     return mass
 
 
@@ -593,9 +596,11 @@ def pa_evict(mass, k_pool, v_pool, block_tables, context_lens, budgets, sink=0, 
     [S, Hkv, W]), packed in order in place or into the blocks of ``new_tables``
     (int32 [S, blocks]).  Returns ``(kept, new_lens, mass_out)``: the kept tokens'
     indices (int32 [S, Hkv, K]), the new lengths (int32 [S]) and the kept tokens'
-    weights (fp32 [S, Hkv, K]); what is past a new length in them is not written.
+    weights; what is past a new length in ``kept`` and ``mass_out`` is not written.
     K comes from ``kept``, or else is ``max_keep`` (default: W), an upper bound of
-    the budgets."""
+    the budgets.  ``mass_out`` may be ``mass`` (evicted weights then stay behind the
+    kept ones: ``own_from_zero`` of the next ``pa_attention_mass``); default: a new
+    fp32 [S, Hkv, W], zero past each new length."""
     torch = _torch()
     dev = mass.device
     desc, seqs, blocks = _batch_args(k_pool, block_tables, context_lens, dev)
@@ -628,7 +633,9 @@ def pa_evict(mass, k_pool, v_pool, block_tables, context_lens, budgets, sink=0, 
     else:
         _arg("new_lens", new_lens, torch.int32, dev, (seqs,))
     if mass_out is None:
-        mass_out = _empty((seqs, hkv, keep), torch.float32, dev, stream)
+        mass_out = _empty((seqs, hkv, width), torch.float32, dev, stream)
+        with torch.cuda.stream(stream):  # (None: the current one)
+            mass_out.zero_()
     else:
         _arg("mass_out", mass_out, torch.float32, dev)
         _dims("mass_out", mass_out, 3)

@@ -33,6 +33,8 @@ PA_KERNEL_SIMT = 1
 PA_KERNEL_TCGEN05 = 2
 PA_PREFILL_EXACT_WEIGHTS = 0x1
 
+PA_MASS_OWN_FROM_ZERO = 0x1
+
 PA_ROPE_HALF = 0
 PA_ROPE_INTERLEAVED = 1
 PA_ROPE_SCALE_NONE = 0
@@ -44,7 +46,7 @@ PA_NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024
 
 # Every entry point of include/pa.h, with its ctypes signature.
 c_int, c_i32, c_i64, c_f32 = ctypes.c_int, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
-c_f64 = ctypes.c_double
+c_f64, c_u32 = ctypes.c_double, ctypes.c_uint32
 c_vp, c_size = ctypes.c_void_p, ctypes.c_size_t
 
 
@@ -112,6 +114,9 @@ SIGNATURES = {
     # eviction (include/pa_evict.h)
     "pa_attention_mass": (c_int, [c_vp, c_i64, c_vp, c_vp, c_i32, c_i32, c_vp, PoolDesc, c_vp, c_i32,
                                   c_vp, c_i32, c_i32, c_f32, c_vp, c_vp, c_i64, c_vp]),
+    "pa_attention_mass_ex": (c_int, [c_vp, c_i64, c_vp, c_vp, c_i32, c_i32, c_vp, PoolDesc, c_vp,
+                                     c_i32, c_vp, c_i32, c_i32, c_f32, c_vp, c_vp, c_i64, c_u32,
+                                     c_vp]),
     "pa_evict": (c_int, [c_vp, c_i64, c_vp, c_vp, PoolDesc, c_vp, c_i32, c_vp, c_vp, c_i32, c_i32,
                          c_vp, c_i32, c_vp, c_i32, c_vp, c_vp, c_i64, c_i32, c_vp]),
     "pa_compact_tokens": (c_int, [c_vp, c_vp, PoolDesc, c_vp, c_i32, c_vp, c_i32, c_vp, c_vp, c_i32,

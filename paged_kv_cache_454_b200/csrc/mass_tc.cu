@@ -92,6 +92,7 @@ struct __align__(64) MassParams {
   int tpt;  // queries of a column tile
   Divisor by_tpt, by_group;
   int num_seqs;
+  int own_from_zero;  // the step's own tokens have no weight in mass_in
   float scale_log2;
 };
 
@@ -509,8 +510,9 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
       }
       const int key = (u.j0 + jj) * 128 + r;
       const int64_t at = (static_cast<int64_t>(u.s) * p.hkv + u.g) * p.mass_stride + key;
-      const float before = p.mass_in && key < q.L ? p.mass_in[at] : 0.f;
       const int rel = key - (q.L - q.n);  // this key among the step's own tokens
+      const float before =
+          p.mass_in && key < q.L && !(p.own_from_zero && rel >= 0) ? p.mass_in[at] : 0.f;
       float sum0 = 0.f, sum1 = 0.f;
       for (int i = i0; i < q.cols; ++i, ++qi, ++steps) {
         const int cols = min(p.tpt, q.n - i * p.tpt) * p.group;
@@ -611,10 +613,22 @@ int pa_attention_mass(const void* q, int64_t q_stride, const float* lse, const i
                       const int32_t* context_lens, int32_t num_seqs, int32_t num_q_heads,
                       float scale, const float* mass_in, float* mass_out, int64_t mass_stride,
                       void* stream) {
+  return pa_attention_mass_ex(q, q_stride, lse, cu_q_lens, total_q, max_q_len, k_pool, pool,
+                              block_tables, max_blocks_per_seq, context_lens, num_seqs, num_q_heads,
+                              scale, mass_in, mass_out, mass_stride, 0, stream);
+}
+
+int pa_attention_mass_ex(const void* q, int64_t q_stride, const float* lse,
+                         const int32_t* cu_q_lens, int32_t total_q, int32_t max_q_len,
+                         const void* k_pool, pa_pool_desc pool, const int32_t* block_tables,
+                         int32_t max_blocks_per_seq, const int32_t* context_lens, int32_t num_seqs,
+                         int32_t num_q_heads, float scale, const float* mass_in, float* mass_out,
+                         int64_t mass_stride, uint32_t flags, void* stream) {
   PA_NVTX_RANGE("pa_attention_mass");
   const int st = check_pool(pool);
   if (st != PA_OK) return st;
-  if (num_seqs < 0 || total_q < 0 || num_q_heads <= 0 || max_blocks_per_seq <= 0 || mass_stride < 0)
+  if (num_seqs < 0 || total_q < 0 || num_q_heads <= 0 || max_blocks_per_seq <= 0 ||
+      mass_stride < 0 || (flags & ~static_cast<uint32_t>(PA_MASS_OWN_FROM_ZERO)))
     return PA_ERR_ARG;
   if (num_q_heads % pool.num_kv_heads) return PA_ERR_SHAPE;
   const int group = num_q_heads / pool.num_kv_heads;
@@ -653,6 +667,7 @@ int pa_attention_mass(const void* q, int64_t q_stride, const float* lse, const i
   p.by_tpt = Divisor(p.tpt);
   p.by_group = Divisor(group);
   p.num_seqs = num_seqs;
+  p.own_from_zero = (flags & PA_MASS_OWN_FROM_ZERO) != 0;
   p.scale_log2 = scale * kLog2e;
   const int64_t tiles = (static_cast<int64_t>(max_blocks_per_seq) * 16 + 127) / 128;
   const int64_t most = tiles > num_sms() ? num_sms() : tiles * num_seqs * p.hkv;

@@ -298,3 +298,11 @@ def test_oracle_compact():
     assert np.array_equal(got[0], pool_[0]) and np.array_equal(got[1], pool_[1])
     far = drafting.compact(pool_, [2, 0], 0, [[17], [0]], new_table=[1])
     assert far[1, 0, 0, 0] == pool_[0, 0, 1, 0] and far[1, 1, 0, 0] == pool_[2, 1, 0, 0]
+
+
+def test_mass_flags_are_checked(lib):
+    def call(flags, seqs=0):
+        return lib.pa_attention_mass_ex(FAKE, 512, FAKE, FAKE, 6, 5, FAKE, pool(), FAKE, 4, FAKE,
+                                        seqs, 4, 1.0, None, FAKE, 64, flags, None)
+    assert call(0) == call(_abi.PA_MASS_OWN_FROM_ZERO) == _abi.PA_OK
+    assert call(2) == call(1 << 31) == _abi.PA_ERR_ARG

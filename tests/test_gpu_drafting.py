@@ -246,3 +246,64 @@ def test_the_chain_in_one_graph():
         assert torch.equal(a, b)
     assert torch.equal(dk[20:], want_k)
     assert pa().pa_get_device_error() == 0
+
+
+@pytest.mark.parametrize("in_place", [True, False], ids=["in_place", "fresh"])
+def test_evict_again_and_again(in_place):
+    # A budget of 64 tokens, two decode steps, down to the budget again: the new tokens'
+    # weights start from 0, whatever an evicted token's or a draft's weight left there.
+    # float64 follows the weights from what the eviction kept; tolerances of
+    # tests/test_gpu_mass.py.
+    import torch
+    m = Model(4)
+    S, width, budget = 3, 12, 64
+    dk = torch.zeros((2 * S * width, HKV, 16, D), dtype=torch.bfloat16, device="cuda")
+    dv = torch.zeros_like(dk)
+    own = np.arange(2 * S * width).reshape(2, S, width)
+    lens = np.array([64, 150, 97])
+    tables = own[0]
+    m.write(m.rows(int(lens.sum())), np.concatenate([np.arange(x) for x in lens]),
+            np.concatenate([tables[s, np.arange(x) // 16] * 16 + np.arange(x) % 16
+                            for s, x in enumerate(lens)]), dk, dv)
+    mass = torch.rand((S, HKV, 16 * width), device="cuda")
+    if in_place:
+        mass[:, :, 152:] = float("nan")  # of tokens not there yet
+    else:
+        for s, x in enumerate(lens):
+            mass[s, :, x:] = 0
+    for turn in range(3):
+        for _ in range(2):
+            dt = H.dev_i32(tables)
+            slots = np.array([tables[s, x // 16] * 16 + x % 16 for s, x in enumerate(lens)])
+            q = m.write(m.rows(S), lens, slots, dk, dv)
+            had = mass.cpu().numpy().astype(np.float64)
+            _, lse = pa().pa_decode(q, dk, dv, dt, H.dev_i32(lens + 1), SCALE, want_lse=True)
+            pa().pa_attention_mass(q, lse, None, 1, dk, dt, H.dev_i32(lens + 1), SCALE, mass_in=mass,
+                                   mass=mass, own_from_zero=in_place)
+            want = drafting.attention_mass(H.host_bits(q), lse.cpu().numpy(), np.arange(S + 1),
+                                           H.host_bits(dk), tables, lens + 1, SCALE)
+            got = mass.cpu().numpy()
+            for s, x in enumerate(lens):
+                had[s, :, x] = 0
+                total = had[s, :, :x + 1] + want[s]
+                assert np.all(np.abs(got[s, :, :x + 1] - total)
+                              <= 8e-5 * want[s] + 2.0 ** -24 * total + 1e-30)
+            lens = lens + 1
+        before = mass.cpu().numpy()
+        new = None if in_place else own[(turn + 1) % 2]
+        kept, nl, out = pa().pa_evict(mass, dk, dv, dt, H.dev_i32(lens), H.dev_i32([budget] * S),
+                                      sink=2, recent=5, mass_out=mass if in_place else None,
+                                      new_tables=None if in_place else H.dev_i32(new),
+                                      max_keep=budget)
+        assert nl.tolist() == [budget] * S and out.shape == mass.shape
+        for s in range(S):
+            for g in range(HKV):
+                want = drafting.evict_choice(before[s, g], int(lens[s]), budget, 2, 5)
+                assert np.array_equal(kept[s, g].cpu().numpy(), want)
+                assert np.array_equal(out[s, g, :budget].cpu().numpy(), before[s, g, want])
+        if not in_place:
+            assert not bool(out[:, :, budget:].any())
+            tables = new
+        mass = out
+        lens = np.full(S, budget)
+    assert pa().pa_get_device_error() == 0
