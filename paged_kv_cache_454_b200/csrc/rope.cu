@@ -161,7 +161,9 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_cons
   __syncthreads();
   if (!live) return;  // whole warps: none takes part in a shuffle below
 
-  // A and B of this lane's dims; dims past rot go through with A = the weight
+  // A and B of this lane's dims; dims past rot go through with A = the weight, or as
+  // they are (a product would flush subnormals and not keep a NaN's bits)
+  const bool as_is = !rotated && !weight;
   float2 A[4], B[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -219,7 +221,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_cons
         const float2 xo = rotated ? unpack2(other) : make_float2(0.f, 0.f);
         float2 y = __ffma2_rn(x, A[j], __fmul2_rn(xo, B[j]));
         if (weight) y = __fmul2_rn(y, make_float2(r, r));
-        o[j] = pack2(y);
+        o[j] = as_is ? own : pack2(y);
       }
       if (h < heads && dst) dst[h * dst_step] = make_uint4(o[0], o[1], o[2], o[3]);
     }

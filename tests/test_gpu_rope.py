@@ -210,3 +210,29 @@ def test_rope_on_a_side_stream_and_in_a_graph():
     g.replay()
     again, _ = pa().pa_rope(x, None, pos, f)
     assert torch.equal(out, again) and not torch.equal(out, want)
+
+
+@pytest.mark.parametrize("d,rot,inter", [(64, 0, False), (64, 48, False), (128, 32, True),
+                                         (128, 0, True), (128, 112, False)])
+def test_dims_past_the_rotation_keep_their_bits(d, rot, inter):
+    # any bits: subnormals, NaN of every payload, both zeros
+    rng = np.random.default_rng(d + rot)
+    t, hq, hkv = 65, 3, 3
+    x = bits(rng, t, hq + 2 * hkv, d)
+    x[..., rot:] = rng.integers(0, 1 << 16, (t, hq + 2 * hkv, d - rot))
+    x[:40, :, rot:] &= 0x807F     # subnormals
+    x[40:50, :, rot:] |= 0x7F80   # infinities and NaN
+    dx, pos, f = H.dev_bf16(x), H.dev_i64(rng.integers(0, 999, t)), dev_f64(freqs(rot))
+    q, k = dx[:, :hq], dx[:, hq:hq + hkv]
+    qo, ko = pa().pa_rope(q, k, pos, f, interleaved=inter, factor=1.5)
+    assert np.array_equal(H.host_bits(qo)[..., rot:], x[:, :hq, rot:])
+    assert np.array_equal(H.host_bits(ko)[..., rot:], x[:, hq:hq + hkv, rot:])
+    dk = H.dev_bf16(np.zeros((5, hkv, 16, d), np.uint16))
+    dv = H.dev_bf16(np.zeros((5, hkv, 16, d), np.uint16))
+    slots = rng.permutation(80)[:t]
+    qo = pa().pa_rope_and_cache(q, k, dx[:, hq + hkv:], dk, dv, H.dev_i64(slots), pos, f,
+                                interleaved=inter, factor=1.5)
+    assert np.array_equal(H.host_bits(qo)[..., rot:], x[:, :hq, rot:])
+    flat = lambda p: np.swapaxes(H.host_bits(p), 1, 2).reshape(-1, hkv, d)  # noqa: E731
+    assert np.array_equal(flat(dk)[slots][..., rot:], x[:, hq:hq + hkv, rot:])
+    assert np.array_equal(flat(dv)[slots], x[:, hq + hkv:])
