@@ -87,7 +87,8 @@ PA_API int pa_rope_and_cache(const void* q, int64_t q_stride, void* q_out, int64
  *                         pair makes over the original context: f_i where r_i >=
  *                         high_turns, f_i / scale where r_i <= low_turns, a linear
  *                         blend of the two between; factor 0.1 ln(scale) + 1 (1
- *                         for scale <= 1).
+ *                         for scale <= 1).  (A checkpoint whose blend is linear in
+ *                         the pair's index i instead needs an array of its own.)
  * low_turns, high_turns and original_max_position are read by
  * PA_ROPE_SCALE_RAMP only.  PA_ERR_ARG on an odd or non-positive rot_dim, a
  * base <= 1, a scale <= 0, or high_turns <= low_turns; PA_ROPE_SCALE_BASE needs

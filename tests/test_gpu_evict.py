@@ -243,3 +243,30 @@ def test_evict_in_a_graph_and_on_a_stream():
     for x, y in ((c, a), (e, a)):
         assert torch.equal(x[1].view(torch.int16), y[1].view(torch.int16))
         assert torch.equal(x[2].view(torch.int16), y[2].view(torch.int16))
+
+
+@pytest.mark.parametrize("length,rows", [(500, 1), (500, 41), (6000, 1), (6000, 41), (36000, 1),
+                                         (133000, 1)])
+def test_every_kept_weight_keeps_its_value(length, rows):
+    # bit by bit, in rows that hold NaN of any payload among infinities, denormals and
+    # zeros: -0 becomes 0, a NaN the canonical one
+    b = Batch(29, [length] + [1] * (rows - 1), 2, 64)
+    pool = np.array([np.inf, -np.inf, 1e-45, 3e-45, -1e-45, 0.0, -0.0, -2.5, 7.0, 1e38], np.float32)
+    m = b.rng.choice(pool, (2, length))
+    nan = (b.rng.integers(1, 1 << 23, (2, length)) | 0x7F800000).astype(np.uint32)
+    nan |= b.rng.integers(0, 2, (2, length)).astype(np.uint32) << 31
+    b.mass[0] = np.where(b.rng.random((2, length)) < 0.3, nan.view(np.float32), m)
+    for budget in (length // 4, length - 5):  # the second keeps some NaN
+        (kept, lens, mass), _, _ = b.run([budget] * rows, 3, 11, True)
+        want = b.choices([budget] * rows, 3, 11, kept.shape[2])
+        got = mass.cpu().numpy()
+        for g in range(2):
+            n = len(want[0][g])
+            assert lens[0] == n
+            assert np.array_equal(kept[0, g, :n].cpu().numpy(), want[0][g])
+            w = b.mass[0, g][want[0][g]]
+            bits = np.where(np.isnan(w), np.uint32(0x7FC00000),
+                            (np.where(np.isnan(w), 0, w) + np.float32(0)).view(np.uint32))
+            assert np.array_equal(got[0, g, :n].view(np.uint32), bits)
+        assert np.isnan(b.mass[0, 0][want[0][0]]).any()
+    assert pa().pa_get_device_error() == 0
