@@ -207,6 +207,10 @@ class KvManager:
             self._release(old)
             s["table"][-1] = fresh
             pairs.append((old, fresh))
+        elif n > 0 and L % self.bs != 0 and s["table"][-1] in self.prefix_of:
+            # share_blocks can leave a full block as a partly used last one: what is
+            # written now is not what it is cached for
+            self._uncache(s["table"][-1])
         slots = []
         for t in tokens:
             if L % self.bs == 0:

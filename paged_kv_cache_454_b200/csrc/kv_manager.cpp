@@ -239,6 +239,10 @@ struct pa_kvm {
       pair[0] = old;
       pair[1] = fresh;
       ++*num_pairs;
+    } else if (n > 0 && L % bs != 0) {
+      // (share_blocks can leave a full block as a partly used last one: what is written
+      // now is not what it is cached for)
+      uncache(s.table.back());
     }
     for (int32_t t = 0; t < n; ++t) {
       if (L % bs == 0) s.table.push_back(alloc());

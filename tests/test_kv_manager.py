@@ -156,3 +156,18 @@ def test_batch_update_tracks_decode_steps():
         m.batch_update(ids, out)
         full = m.batch(ids, 12)
         assert np.array_equal(out[0], full[0]) and np.array_equal(out[1], full[1]), step
+
+
+@pytest.mark.parametrize("make", [oracle.KvManager, KvManager], ids=["oracle", "library"])
+def test_a_cached_block_that_is_written_into_leaves_the_cache(make):
+    # the last holder of a shared full block, which uses only its first rows, writes on
+    # in place: the block no longer holds what it was cached for
+    m = make(16, 4, True)
+    m.add_sequence(0, list(range(8)))
+    m.add_sequence(1, [50, 51, 52, 53, 54])
+    m.share_blocks(0, 1, [1])                    # its second block, one row of it in use
+    m.free_sequence(0)
+    table = m.block_table(1)
+    slots, pairs = m.append_tokens(1, [60])
+    assert [int(s) for s in slots] == [table[1] * 4 + 1] and not pairs
+    assert m.add_sequence(2, list(range(8)) + [1])[1] == 4  # the first block only
