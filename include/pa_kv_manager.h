@@ -112,6 +112,41 @@ PA_API int pa_kvm_decode_step(pa_kvm* m, const int64_t* seq_ids, int32_t num_seq
                               const int32_t* tokens, int64_t* slots, int64_t* copy_pairs,
                               int32_t* num_pairs);
 
+/*
+ * Drafted and evicted sequences.  Token ids identify a block's contents in the prefix
+ * cache, and neither a draft nor an evicted cache can be told by them: a tree's tokens
+ * are moved about when a branch is accepted, and after an eviction a slot holds another
+ * token for every KV head.
+ *
+ * pa_kvm_append_draft -- reserve the slots of n >= 0 drafted tokens behind a sequence
+ * (slots, copy_pair and num_pairs as in pa_kvm_append_tokens; nothing is cached).  The
+ * length counts them, as pa_tree_attention has it.  Until they are accepted the sequence
+ * can only be accepted, freed or inspected (PA_ERR_ARG from the others).
+ *
+ * pa_kvm_accept_draft -- the first n of the draft's slots now hold `tokens` (int32 [n],
+ * may be NULL when prefix caching is off), to where pa_compact_tokens moves the accepted
+ * branch; the rest is dropped and the blocks that only it needed are released, last
+ * first.  n = 0 drops the whole draft.  PA_ERR_ARG for n beyond the draft.
+ *
+ * pa_kvm_add_reserved -- a new sequence of n >= 0 tokens in fresh blocks that nothing
+ * describes: the new_tables of pa_evict.  Nothing of it is looked up in the prefix cache
+ * or put there, then or later.
+ *
+ * pa_kvm_evicted -- a sequence was brought down to its first n rows in place (pa_evict
+ * without new_tables): the blocks past them are released, last first, the others leave
+ * the prefix cache with every cached block whose prefix runs through them, and from now
+ * on the sequence is as one of pa_kvm_add_reserved.  To be called before the blocks'
+ * next lookup.  PA_ERR_ARG if another table holds one of the first ceil(n / block_size)
+ * blocks (such a sequence has to be packed into fresh blocks).
+ *
+ * pa_kvm_share_blocks refuses a reserved or evicted sequence on either side.
+ */
+PA_API int pa_kvm_append_draft(pa_kvm* m, int64_t seq_id, int32_t n, int64_t* slots,
+                               int64_t* copy_pair, int32_t* num_pairs);
+PA_API int pa_kvm_accept_draft(pa_kvm* m, int64_t seq_id, const int32_t* tokens, int32_t n);
+PA_API int pa_kvm_add_reserved(pa_kvm* m, int64_t seq_id, int32_t n);
+PA_API int pa_kvm_evicted(pa_kvm* m, int64_t seq_id, int32_t n);
+
 /* pa_kvm_fork -- new sequence `child` sharing every block of `parent`. */
 PA_API int pa_kvm_fork(pa_kvm* m, int64_t parent, int64_t child);
 

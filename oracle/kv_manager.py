@@ -59,6 +59,11 @@ Readings taken where the pages are silent or leave a choice:
   are released (last first; cached ones stay cached) and the table lists host
   blocks; swapping in takes fresh device blocks (registering nothing in the
   prefix cache).  A swapped-out sequence can only be swapped in or freed.
+* Token ids say what a block holds, in the cache; a draft and an evicted cache cannot
+  be told by them.  A draft's slots are appended without ids (and until it is accepted
+  the sequence can only be accepted, freed or inspected), its accepted tokens get theirs
+  when it ends.  A reserved or evicted sequence is never in the cache, its blocks leave
+  it, and it takes part in no ``share_blocks``.
 * Every operation is all-or-nothing: when the pool cannot supply the blocks it
   needs, it raises ``NoBlocks`` and changes nothing.
 """
@@ -155,6 +160,20 @@ class KvManager:
             raise KvManagerError(f"sequence {sid} is swapped out")
         return s
 
+    def _settled(self, sid):
+        s = self._seq(sid)
+        if s.get("draft"):
+            raise KvManagerError(f"sequence {sid} has an open draft")
+        return s
+
+    def _cut(self, s, n):
+        """Drop the blocks that the first ``n`` tokens do not need, last first."""
+        keep = -(-n // self.bs)
+        for b in reversed(s["table"][keep:]):
+            self._release(b)
+        del s["table"][keep:]
+        s["len"] = n
+
     # ------------------------------------------------------------- sequences
     def add_sequence(self, sid, tokens):
         """A new sequence with prompt ``tokens``.  Returns (slots, cached_tokens)."""
@@ -192,8 +211,9 @@ class KvManager:
     def append_tokens(self, sid, tokens):
         """Reserve slots for ``tokens`` at the end of the sequence.
         Returns (slots, copy_pairs)."""
-        s = self._seq(sid)
-        tokens = [int(t) for t in tokens]
+        return self._append(self._settled(sid), [int(t) for t in tokens])
+
+    def _append(self, s, tokens):
         n = len(tokens)
         L = s["len"]
         # blocks needed: copy of a shared partial last block, then fresh blocks
@@ -216,12 +236,63 @@ class KvManager:
             if L % self.bs == 0:
                 s["table"].append(self._alloc())
             slots.append(s["table"][L // self.bs] * self.bs + L % self.bs)
-            s["tokens"].append(t)
+            if t is not None and not s.get("opaque"):
+                self._name(s, L, t)
             L += 1
-            if L % self.bs == 0:
-                self._register(s["table"][L // self.bs - 1], tuple(s["tokens"][:L]))
         s["len"] = L
         return slots, pairs
+
+    def _name(self, s, at, token):
+        """Token ``at`` (the next one) is ``token``; a block that is full with it may be
+        cached."""
+        s["tokens"].append(token)
+        if (at + 1) % self.bs == 0:
+            self._register(s["table"][at // self.bs], tuple(s["tokens"][:at + 1]))
+
+    # ------------------------------------------------- drafts and evicted caches
+    def append_draft(self, sid, n):
+        """Slots for ``n`` drafted tokens.  Returns (slots, copy_pairs)."""
+        s = self._settled(sid)
+        if n < 0:
+            raise KvManagerError("a negative draft")
+        res = self._append(s, [None] * n)
+        s["draft"] = n
+        return res
+
+    def accept_draft(self, sid, tokens):
+        """The first slots of the draft hold ``tokens``; the rest is dropped."""
+        s = self._seq(sid)
+        n = len(tokens)
+        if n > s.get("draft", 0):
+            raise KvManagerError("more tokens than were drafted")
+        base = s["len"] - s.get("draft", 0)
+        self._cut(s, base + n)
+        s["draft"] = 0
+        if not s.get("opaque"):
+            for i, t in enumerate(tokens):
+                self._name(s, base + i, int(t))
+
+    def add_reserved(self, sid, n):
+        """A new sequence of ``n`` tokens in fresh blocks, never in the cache."""
+        if sid in self.seqs or n < 0:
+            raise KvManagerError(f"duplicate sequence {sid} or a negative length")
+        self._need(-(-n // self.bs))
+        table = [self._alloc() for _ in range(-(-n // self.bs))]
+        self.seqs[sid] = {"table": table, "len": n, "tokens": [], "opaque": True}
+
+    def evicted(self, sid, n):
+        """The sequence was brought down to its first ``n`` rows in place."""
+        s = self._settled(sid)
+        if n < 0 or n > s["len"]:
+            raise KvManagerError("a length beyond the sequence")
+        kept = s["table"][:-(-n // self.bs)]
+        if any(self.ref[b] != 1 for b in kept):
+            raise KvManagerError("another table holds one of the blocks")
+        for b in kept:
+            if b in self.prefix_of:
+                self._uncache(b)
+        self._cut(s, n)
+        s["opaque"], s["tokens"] = True, []
 
     def decode_step(self, sids, tokens):
         """One new token for each of ``sids`` (in order), all or nothing.
@@ -230,7 +301,7 @@ class KvManager:
             raise KvManagerError("a sequence listed twice")
         need, drops = 0, {}
         for sid in sids:
-            st = self._seq(sid)
+            st = self._settled(sid)
             L = st["len"]
             if L % self.bs == 0:
                 need += 1
@@ -249,15 +320,16 @@ class KvManager:
 
     def fork(self, parent, child):
         """Whole-sequence sharing: ``child`` holds every block of ``parent``."""
-        p = self._seq(parent)
+        p = self._settled(parent)
         if child in self.seqs:
             raise KvManagerError(f"duplicate sequence {child}")
         for b in p["table"]:
             self._retain(b)
-        self.seqs[child] = {"table": list(p["table"]), "len": p["len"], "tokens": list(p["tokens"])}
+        self.seqs[child] = {"table": list(p["table"]), "len": p["len"], "tokens": list(p["tokens"]),
+                            "opaque": p.get("opaque", False)}
 
     def share_prefix(self, src, dst, n_blocks):
-        s = self._seq(src)
+        s = self._settled(src)
         if dst in self.seqs:
             raise KvManagerError(f"duplicate sequence {dst}")
         if n_blocks < 0 or n_blocks > len(s["table"]):
@@ -266,10 +338,12 @@ class KvManager:
         for b in s["table"][:n_blocks]:
             self._retain(b)
         self.seqs[dst] = {"table": list(s["table"][:n_blocks]), "len": L,
-                          "tokens": list(s["tokens"][:L])}
+                          "tokens": list(s["tokens"][:L]), "opaque": s.get("opaque", False)}
 
     def share_blocks(self, src, dst, idx):
-        s, d = self._seq(src), self._seq(dst)
+        s, d = self._settled(src), self._settled(dst)
+        if s.get("opaque") or d.get("opaque"):
+            raise KvManagerError("no token ids say what the blocks hold")
         idx = [int(i) for i in idx]
         for i in idx:
             if i < 0 or (i + 1) * self.bs > s["len"] or i >= len(d["table"]):
@@ -298,7 +372,7 @@ class KvManager:
         """Move a sequence's blocks to host blocks ("当大模型推理遇上内存瓶颈" 5.1,
         7.3).  Only a sequence that holds all its blocks alone can move.
         Returns the (device, host) pairs to copy."""
-        s = self._seq(sid)
+        s = self._settled(sid)
         if any(self.ref[b] != 1 for b in s["table"]):
             raise KvManagerError("a shared block cannot be swapped out")
         if len(s["table"]) > len(self.host_free):

@@ -97,6 +97,10 @@ SIGNATURES = {
     "pa_kvm_swap_out": (c_int, [c_vp, c_i64, c_vp, c_i32, c_vp]),
     "pa_kvm_swap_in": (c_int, [c_vp, c_i64, c_vp, c_i32, c_vp]),
     "pa_kvm_num_free_host_blocks": (c_i32, [c_vp]),
+    "pa_kvm_append_draft": (c_int, [c_vp, c_i64, c_i32, c_vp, c_vp, ctypes.POINTER(c_i32)]),
+    "pa_kvm_accept_draft": (c_int, [c_vp, c_i64, c_vp, c_i32]),
+    "pa_kvm_add_reserved": (c_int, [c_vp, c_i64, c_i32]),
+    "pa_kvm_evicted": (c_int, [c_vp, c_i64, c_i32]),
     # block swapping (include/pa_swap.h)
     "pa_swap_blocks": (c_int, [c_vp, c_vp, PoolDesc, c_vp, c_vp, c_i32, c_vp, c_i32, c_i32, c_vp]),
     # rotary positions, head norms and the cache write (include/pa_rope.h)

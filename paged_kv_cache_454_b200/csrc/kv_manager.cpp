@@ -87,6 +87,8 @@ struct Seq {
   int32_t len = 0;
   uint64_t stamp = 0;           // last batch call that listed this sequence
   bool swapped = false;         // table lists host swap-space blocks
+  int32_t draft = 0;            // of len: drafted tokens, neither accepted nor dropped yet
+  bool opaque = false;          // no token ids say what the blocks hold: never cached
   std::vector<int32_t> tokens;  // kept only with prefix caching
   std::vector<uint64_t> hash;   // chain hash of each full block (prefix caching)
 };
@@ -123,6 +125,12 @@ struct pa_kvm {
   Seq* resident(int64_t id) {
     auto it = seqs.find(id);
     return it == seqs.end() || it->second.swapped ? nullptr : &it->second;
+  }
+
+  // The same, without an open draft.
+  Seq* settled(int64_t id) {
+    Seq* s = resident(id);
+    return s && s->draft == 0 ? s : nullptr;
   }
 
   int32_t num_free() const { return free_set.size() + n_lru; }
@@ -227,7 +235,29 @@ struct pa_kvm {
     return (s.len + n + bs - 1) / bs - (s.len + bs - 1) / bs + (*cow ? 1 : 0);
   }
 
-  // Append n tokens to s; the caller has checked the pool can supply the blocks.
+  // Token L of s (the next one) is `token`: with its block's last one, that block is
+  // full and may be cached.
+  void name_token(Seq& s, int32_t L, int32_t token) {
+    s.tokens.push_back(token);
+    if ((L + 1) % bs != 0) return;
+    const int32_t k = L / bs;
+    const uint64_t parent = parent_hash(s, k);
+    const uint64_t h = chain_hash(parent, s.tokens.data() + k * bs, bs);
+    s.hash.push_back(h);
+    reg(s.table[k], k, h, parent, s.tokens.data() + k * bs);
+  }
+
+  // The table of s without the blocks that n tokens do not need, last block first.
+  void cut(Seq& s, int32_t n) {
+    while (static_cast<int32_t>(s.table.size()) > (n + bs - 1) / bs) {
+      release(s.table.back());
+      s.table.pop_back();
+    }
+    s.len = n;
+  }
+
+  // Append n tokens to s (without ids where `tokens` is null); the caller has checked
+  // the pool can supply the blocks.
   void append(Seq& s, const int32_t* tokens, int32_t n, bool cow, int64_t* slots,
               int64_t* pair, int32_t* num_pairs) {
     int32_t L = s.len;
@@ -247,15 +277,8 @@ struct pa_kvm {
     for (int32_t t = 0; t < n; ++t) {
       if (L % bs == 0) s.table.push_back(alloc());
       slots[t] = static_cast<int64_t>(s.table[L / bs]) * bs + L % bs;
-      if (pc) s.tokens.push_back(tokens[t]);
+      if (pc && tokens && !s.opaque) name_token(s, L, tokens[t]);
       ++L;
-      if (pc && L % bs == 0) {
-        const int32_t k = L / bs - 1;
-        const uint64_t parent = parent_hash(s, k);
-        const uint64_t h = chain_hash(parent, s.tokens.data() + k * bs, bs);
-        s.hash.push_back(h);
-        reg(s.table[k], k, h, parent, s.tokens.data() + k * bs);
-      }
     }
     s.len = L;
   }
@@ -336,7 +359,7 @@ PA_API int pa_kvm_append_tokens(pa_kvm* m, int64_t seq_id, const int32_t* tokens
                                 int64_t* slots, int64_t* copy_pair, int32_t* num_pairs) {
   if (!m || n < 0 || (n > 0 && !slots) || (m->pc && n > 0 && !tokens) || !num_pairs)
     return PA_ERR_ARG;
-  Seq* sp = m->resident(seq_id);
+  Seq* sp = m->settled(seq_id);
   if (!sp) return PA_ERR_ARG;
   Seq& s = *sp;
   *num_pairs = 0;
@@ -346,6 +369,64 @@ PA_API int pa_kvm_append_tokens(pa_kvm* m, int64_t seq_id, const int32_t* tokens
   if (cow && !copy_pair) return PA_ERR_ARG;
   if (need > m->num_free()) return PA_ERR_NO_BLOCKS;
   m->append(s, tokens, n, cow, slots, copy_pair, num_pairs);
+  return PA_OK;
+}
+
+PA_API int pa_kvm_append_draft(pa_kvm* m, int64_t seq_id, int32_t n, int64_t* slots,
+                               int64_t* copy_pair, int32_t* num_pairs) {
+  if (!m || n < 0 || (n > 0 && !slots) || !num_pairs) return PA_ERR_ARG;
+  Seq* s = m->settled(seq_id);
+  if (!s) return PA_ERR_ARG;
+  *num_pairs = 0;
+  if (n == 0) return PA_OK;
+  if (n > static_cast<int64_t>(m->nb) * m->bs - s->len) return PA_ERR_NO_BLOCKS;
+  bool cow = false;
+  const int32_t need = m->blocks_needed(*s, n, &cow);
+  if (cow && !copy_pair) return PA_ERR_ARG;
+  if (need > m->num_free()) return PA_ERR_NO_BLOCKS;
+  m->append(*s, nullptr, n, cow, slots, copy_pair, num_pairs);
+  s->draft = n;
+  return PA_OK;
+}
+
+PA_API int pa_kvm_accept_draft(pa_kvm* m, int64_t seq_id, const int32_t* tokens, int32_t n) {
+  if (!m || n < 0) return PA_ERR_ARG;
+  Seq* s = m->resident(seq_id);
+  if (!s || n > s->draft || (m->pc && !s->opaque && n > 0 && !tokens)) return PA_ERR_ARG;
+  const int32_t base = s->len - s->draft;
+  m->cut(*s, base + n);
+  if (m->pc && !s->opaque)
+    for (int32_t t = 0; t < n; ++t) m->name_token(*s, base + t, tokens[t]);
+  s->draft = 0;
+  return PA_OK;
+}
+
+PA_API int pa_kvm_add_reserved(pa_kvm* m, int64_t seq_id, int32_t n) {
+  if (!m || n < 0 || m->seqs.count(seq_id)) return PA_ERR_ARG;
+  if (n > static_cast<int64_t>(m->nb) * m->bs) return PA_ERR_NO_BLOCKS;
+  const int32_t blocks = static_cast<int32_t>((static_cast<int64_t>(n) + m->bs - 1) / m->bs);
+  if (blocks > m->num_free()) return PA_ERR_NO_BLOCKS;
+  Seq s;
+  s.table.reserve(blocks);
+  for (int32_t i = 0; i < blocks; ++i) s.table.push_back(m->alloc());
+  s.len = n;
+  s.opaque = true;
+  m->seqs.emplace(seq_id, std::move(s));
+  return PA_OK;
+}
+
+PA_API int pa_kvm_evicted(pa_kvm* m, int64_t seq_id, int32_t n) {
+  if (!m || n < 0) return PA_ERR_ARG;
+  Seq* s = m->settled(seq_id);
+  if (!s || n > s->len) return PA_ERR_ARG;
+  const int32_t blocks = (n + m->bs - 1) / m->bs;
+  for (int32_t i = 0; i < blocks; ++i)
+    if (m->ref[s->table[i]] != 1) return PA_ERR_ARG;  // another table holds it
+  for (int32_t i = 0; i < blocks; ++i) m->uncache(s->table[i]);
+  m->cut(*s, n);
+  s->opaque = true;
+  s->tokens.clear();
+  s->hash.clear();
   return PA_OK;
 }
 
@@ -362,7 +443,9 @@ PA_API int pa_kvm_decode_step(pa_kvm* m, const int64_t* seq_ids, int32_t num_seq
   int32_t need = 0;
   for (int32_t i = 0; i < num_seqs; ++i) {
     auto it = m->seqs.find(seq_ids[i]);
-    if (it == m->seqs.end() || it->second.swapped || it->second.stamp == stamp) return PA_ERR_ARG;
+    if (it == m->seqs.end() || it->second.swapped || it->second.draft > 0 ||
+        it->second.stamp == stamp)
+      return PA_ERR_ARG;
     Seq& s = it->second;
     s.stamp = stamp;
     ss[i] = &s;
@@ -391,7 +474,7 @@ PA_API int pa_kvm_decode_step(pa_kvm* m, const int64_t* seq_ids, int32_t num_seq
 
 PA_API int pa_kvm_fork(pa_kvm* m, int64_t parent, int64_t child) {
   if (!m) return PA_ERR_ARG;
-  Seq* p = m->resident(parent);
+  Seq* p = m->settled(parent);
   if (!p || m->seqs.count(child)) return PA_ERR_ARG;
   Seq c = *p;
   for (int32_t b : c.table) m->retain(b);
@@ -401,14 +484,15 @@ PA_API int pa_kvm_fork(pa_kvm* m, int64_t parent, int64_t child) {
 
 PA_API int pa_kvm_share_prefix(pa_kvm* m, int64_t src, int64_t dst, int32_t n_blocks) {
   if (!m) return PA_ERR_ARG;
-  const Seq* sp = m->resident(src);
+  const Seq* sp = m->settled(src);
   if (!sp || m->seqs.count(dst)) return PA_ERR_ARG;
   const Seq& s = *sp;
   if (n_blocks < 0 || n_blocks > static_cast<int32_t>(s.table.size())) return PA_ERR_ARG;
   Seq d;
   d.len = std::min(s.len, n_blocks * m->bs);
   d.table.assign(s.table.begin(), s.table.begin() + n_blocks);
-  if (m->pc) {
+  d.opaque = s.opaque;
+  if (m->pc && !s.opaque) {
     d.tokens.assign(s.tokens.begin(), s.tokens.begin() + d.len);
     d.hash.assign(s.hash.begin(), s.hash.begin() + d.len / m->bs);
   }
@@ -419,9 +503,9 @@ PA_API int pa_kvm_share_prefix(pa_kvm* m, int64_t src, int64_t dst, int32_t n_bl
 
 PA_API int pa_kvm_share_blocks(pa_kvm* m, int64_t src, int64_t dst, const int32_t* idx, int32_t n) {
   if (!m || n < 0 || (n > 0 && !idx)) return PA_ERR_ARG;
-  Seq* sp = m->resident(src);
-  Seq* dp = m->resident(dst);
-  if (!sp || !dp) return PA_ERR_ARG;
+  Seq* sp = m->settled(src);
+  Seq* dp = m->settled(dst);
+  if (!sp || !dp || sp->opaque || dp->opaque) return PA_ERR_ARG;
   Seq& s = *sp;
   Seq& d = *dp;
   const int32_t bs = m->bs;
@@ -522,7 +606,7 @@ PA_API int pa_kvm_batch_update(const pa_kvm* m, const int64_t* seq_ids, int32_t 
 PA_API int pa_kvm_swap_out(pa_kvm* m, int64_t seq_id, int64_t* pairs, int32_t capacity,
                            int32_t* num_pairs) {
   if (!m || capacity < 0 || !num_pairs || (capacity > 0 && !pairs)) return PA_ERR_ARG;
-  Seq* sp = m->resident(seq_id);
+  Seq* sp = m->settled(seq_id);
   if (!sp) return PA_ERR_ARG;
   Seq& s = *sp;
   const int32_t n = static_cast<int32_t>(s.table.size());

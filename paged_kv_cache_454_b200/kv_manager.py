@@ -90,6 +90,30 @@ class KvManager:
                                                    _p(pair), ctypes.byref(npairs)))
         return slots, [(int(pair[0]), int(pair[1]))] if npairs.value else []
 
+    def append_draft(self, seq_id: int, n: int):
+        """Slots for ``n`` drafted tokens; returns what ``append_tokens`` returns."""
+        slots = np.empty(max(int(n), 0), np.int64)
+        pair = np.empty(2, np.int64)
+        npairs = ctypes.c_int32(0)
+        self._check("pa_kvm_append_draft",
+                    self._lib.pa_kvm_append_draft(self._h, seq_id, n, _p(slots), _p(pair),
+                                                  ctypes.byref(npairs)))
+        return slots, [(int(pair[0]), int(pair[1]))] if npairs.value else []
+
+    def accept_draft(self, seq_id: int, tokens):
+        """The draft's first slots hold ``tokens`` now, the rest of it is dropped."""
+        t = _i32(tokens)
+        self._check("pa_kvm_accept_draft",
+                    self._lib.pa_kvm_accept_draft(self._h, seq_id, _p(t), len(t)))
+
+    def add_reserved(self, seq_id: int, n: int):
+        """A new sequence of ``n`` tokens in fresh blocks, outside the prefix cache."""
+        self._check("pa_kvm_add_reserved", self._lib.pa_kvm_add_reserved(self._h, seq_id, n))
+
+    def evicted(self, seq_id: int, n: int):
+        """The sequence was brought down to its first ``n`` rows in place."""
+        self._check("pa_kvm_evicted", self._lib.pa_kvm_evicted(self._h, seq_id, n))
+
     def decode_step(self, seq_ids, tokens, slots=None):
         """One new token per sequence, all or nothing.  Returns (slots int64[S],
         copy pairs as a list of (src, dst)); ``slots`` may be given to fill."""

@@ -307,3 +307,115 @@ def test_evict_again_and_again(in_place):
         mass = out
         lens = np.full(S, budget)
     assert pa().pa_get_device_error() == 0
+
+
+def test_the_block_manager_carries_drafts_and_evictions():
+    # prefix caching on, one prompt for two sequences: a tree each, its accepted branch, a
+    # decode step; then one sequence packed into fresh blocks, the other in place, another
+    # step; at last the prompt again, whose cached blocks must still hold it
+    import torch
+    from paged_kv_cache_454_b200.kv_manager import KvManager
+    m = Model(5)
+    mgr = KvManager(80, prefix_caching=True)
+    dk = torch.zeros((80, HKV, 16, D), dtype=torch.bfloat16, device="cuda")
+    dv = torch.zeros_like(dk)
+    P, width = 70, 8
+    prompt = np.arange(1000, 1000 + P, dtype=np.int32)
+    rows = m.rows(P)
+    for s in range(2):
+        slots, cached = mgr.add_sequence(s, prompt)
+        assert cached == (0, 64)[s]
+        m.write(rows, np.arange(P), slots, dk, dv)
+    k0, v0 = m.prepared(rows, np.arange(P))[1:]
+    bits, depth = [1, 3, 5, 0b1011], np.array([0, 1, 1, 2])
+    n, branches = 4, [[0, 1, 3], [0, 2]]
+    drafts, slots = [m.rows(n) for _ in range(2)], []
+    for s in range(2):
+        sl, pairs = mgr.append_draft(s, n)
+        if pairs:
+            pa().pa_copy_blocks(dk, dv, pairs)
+        slots.append(sl)
+    pos = np.tile(P + depth, 2)
+    q = m.write(np.concatenate(drafts), pos, np.concatenate(slots), dk, dv)
+    tables, ctx = mgr.batch([0, 1], width)
+    assert ctx.tolist() == [P + n] * 2
+    dt = H.dev_i32(tables)
+    out, _ = pa().pa_tree_attention(q, H.dev_i32([0, n, 2 * n]), n,
+                                    H.dev_i64(np.array(bits * 2)[:, None]), dk, dv, dt,
+                                    H.dev_i32(ctx), SCALE)
+    kept = np.zeros((2, 1, 3), np.int32)
+    for s, br in enumerate(branches):
+        kept[s, 0, :len(br)] = br
+    pa().pa_compact_tokens(dk, dv, dt, H.dev_i32(kept), H.dev_i32([3, 2]), base=H.dev_i32([P, P]))
+    kv = []
+    for s, br in enumerate(branches):
+        mgr.accept_draft(s, 2000 + 10 * s + np.array(br))
+        qd, kd, vd = m.prepared(drafts[s], P + depth)
+        for i in range(n):
+            see = [j for j in range(n) if (bits[i] >> j) & 1]
+            close(out[s * n + i], attend(qd[i], np.concatenate([k0, kd[see]]),
+                                         np.concatenate([v0, vd[see]])))
+        kv.append((np.concatenate([k0, kd[br]]), np.concatenate([v0, vd[br]])))
+    lens = np.array([P + 3, P + 2])
+
+    def step(ids, positions, rows_of):
+        """A decode step of sequences ``ids``; ``rows_of(s, g)``: K and V rows head g of
+        sequence s attends to besides its own new one."""
+        r = m.rows(2)
+        sl, pairs = mgr.decode_step(ids, [7, 7])
+        assert not pairs
+        qd = m.write(r, positions, sl, dk, dv)
+        tables, ctx = mgr.batch(ids, width)
+        out, lse = pa().pa_decode(qd, dk, dv, H.dev_i32(tables), H.dev_i32(ctx), SCALE,
+                                  want_lse=True)
+        qn, kn, vn = m.prepared(r, positions)
+        for s in range(2):
+            for g in range(HKV):
+                k, v = rows_of(s, g)
+                for h in range(4 * g, 4 * g + 4):
+                    o, _ = oracle.attend(qn[s, h], np.concatenate([k, kn[s:s + 1, g]]),
+                                         np.concatenate([v, vn[s:s + 1, g]]), SCALE)
+                    assert np.abs(H.host_f64(out[s, h]) - o).max() < 0.06
+            kv[s] = np.concatenate([kv[s][0], kn[s:s + 1]]), np.concatenate([kv[s][1], vn[s:s + 1]])
+        return qd, lse, tables, ctx
+
+    qd, lse, tables, ctx = step([0, 1], lens, lambda s, g: (kv[s][0][:, g], kv[s][1][:, g]))
+    assert ctx.tolist() == [P + 4, P + 3]
+    mass = pa().pa_attention_mass(qd, lse, None, 1, dk, H.dev_i32(tables), H.dev_i32(ctx), SCALE)
+    # sequence 0 into fresh blocks; 1 in place, which its blocks, still the prompt's, forbid
+    mgr.add_reserved(10, 40)
+    fresh, _ = mgr.batch([10], width)
+    kept0, _, _ = pa().pa_evict(mass[:1], dk, dv, H.dev_i32(tables[:1]), H.dev_i32(ctx[:1]),
+                                H.dev_i32([40]), sink=2, recent=8, new_tables=H.dev_i32(fresh))
+    from paged_kv_cache_454_b200.kv_manager import KvManagerError
+    with pytest.raises(KvManagerError):
+        mgr.evicted(1, 40)
+    mgr.add_reserved(11, 50)
+    fresh, _ = mgr.batch([11], width)
+    kept1, _, mass1 = pa().pa_evict(mass[1:].contiguous(), dk, dv, H.dev_i32(tables[1:]),
+                                    H.dev_i32(ctx[1:]), H.dev_i32([50]), sink=2, recent=8,
+                                    new_tables=H.dev_i32(fresh))
+    mgr.free_sequence(0)
+    mgr.free_sequence(1)
+    # the second one once more, now in place: its blocks are its own
+    again, _, _ = pa().pa_evict(mass1, dk, dv, H.dev_i32(fresh), H.dev_i32([50]), H.dev_i32([30]),
+                                sink=1, recent=4, max_keep=30)
+    mgr.evicted(11, 30)
+    idx = [kept0[0, :, :40].cpu().numpy(),
+           np.take_along_axis(kept1[0, :, :50].cpu().numpy(), again[0].cpu().numpy(), 1)]
+    full = list(kv)
+    step([10, 11], np.array([P + 4, P + 3]),
+         lambda s, g: (full[s][0][idx[s][g], g], full[s][1][idx[s][g], g]))
+    assert mgr.context_len(10) == 41 and mgr.context_len(11) == 31
+    # the prompt is still found, and still there
+    slots, cached = mgr.add_sequence(20, prompt)
+    assert cached == 64
+    m.write(rows, np.arange(P), slots, dk, dv)
+    r = m.rows(1)
+    sl, _ = mgr.decode_step([20], [9])
+    qn = m.write(r, np.array([P]), sl, dk, dv)
+    tables, ctx = mgr.batch([20], width)
+    out, _ = pa().pa_decode(qn, dk, dv, H.dev_i32(tables), H.dev_i32(ctx), SCALE)
+    qx, kx, vx = m.prepared(r, np.array([P]))
+    close(out[0], attend(qx[0], np.concatenate([k0, kx]), np.concatenate([v0, vx])))
+    assert pa().pa_get_device_error() == 0
