@@ -419,3 +419,49 @@ def test_the_block_manager_carries_drafts_and_evictions():
     qx, kx, vx = m.prepared(r, np.array([P]))
     close(out[0], attend(qx[0], np.concatenate([k0, kx]), np.concatenate([v0, vx])))
     assert pa().pa_get_device_error() == 0
+
+
+def test_blocks_past_2_to_the_31_elements():
+    # a pool of 4.4 GB: the same calls on blocks at its end and on a small pool, bit by bit
+    import torch
+    S, L, n, hkv = 2, 200, 5, 8
+    per = hkv * 16 * D
+    nb = 2 ** 31 // per + 64
+    need = -(-L // 16)
+    far = nb - 1 - np.random.default_rng(1).permutation(60)[:4 * need // 2 * 2].reshape(2, S, -1)
+    assert far.min() * per > 2 ** 31 - 64 * per and (far * per).max() > 2 ** 31
+    near = np.arange(far.size).reshape(far.shape)
+    big = [torch.empty((nb, hkv, 16, D), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    small = [torch.empty((far.size, hkv, 16, D), dtype=torch.bfloat16, device="cuda")
+             for _ in range(2)]
+    m = Model(6)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    x = torch.randn((S * L, 2 * hkv + 16, D), generator=g, device="cuda", dtype=torch.bfloat16)
+    pos = H.dev_i64(np.tile(np.arange(L), S))
+    cu = H.dev_i32(n * np.arange(S + 1))
+    mask = H.dev_i64(np.tile([(1 << (i + 1)) - 1 for i in range(n)], S)[:, None])
+    lens, f = H.dev_i32([L] * S), dev_f64(m.f)
+    t = np.arange(L)
+    rows = torch.tensor([s * L + L - n + i for s in range(S) for i in range(n)], device="cuda")
+
+    def run(pools, blocks):
+        k, v = pools
+        ids = torch.as_tensor(blocks[1].reshape(-1), device="cuda")
+        k[ids] = 0
+        v[ids] = 0
+        slots = np.concatenate([blocks[0, s, t // 16].astype(np.int64) * 16 + t % 16
+                                for s in range(S)])
+        q = pa().pa_rope_and_cache(x[:, :16], x[:, 16:16 + hkv], x[:, 16 + hkv:], k, v,
+                                   H.dev_i64(slots), pos, f)[rows]
+        tables, new = H.dev_i32(blocks[0]), H.dev_i32(blocks[1])
+        out, lse = pa().pa_tree_attention(q, cu, n, mask, k, v, tables, lens, SCALE, want_lse=True)
+        mass = pa().pa_attention_mass(q, lse, cu, n, k, tables, lens, SCALE)
+        kept, _, w = pa().pa_evict(mass, k, v, tables, lens, H.dev_i32([90] * S), sink=2, recent=9,
+                                   new_tables=new, max_keep=90)
+        pa().pa_compact_tokens(k, v, new, H.dev_i32([[[3, 4, 9]]] * S), H.dev_i32([3] * S),
+                               base=H.dev_i32([50] * S))
+        return out, lse, mass[..., :L], kept, w[..., :90], k[ids], v[ids]
+
+    for a, b in zip(run(big, far), run(small, near)):
+        assert torch.equal(a, b)
+    assert pa().pa_get_device_error() == 0

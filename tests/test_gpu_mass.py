@@ -307,3 +307,30 @@ def test_weights_of_an_accepted_branch(hq, hkv, d):
     # a row's weights sum to 1: each is off by its score's error and the lse's, 8e-5 together
     assert float((mass.sum(2) - m * (hq // hkv)).abs().max()) <= 1e-4 * m * (hq // hkv)
     assert pa().pa_get_device_error() == 0
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(16, 2, 128), (3, 3, 64)])
+def test_weights_of_a_whole_prompt(hq, hkv, d):
+    # every query of 4500 tokens; a token's two sums take up to 4500 * G / 2 terms each,
+    # rounded after each: 2^-24 of W for every one, and 8e-5 W as above
+    import torch
+    n = 4500
+    g = torch.Generator(device="cuda").manual_seed(d)
+    rand = lambda *shape: torch.randn(shape, generator=g, device="cuda",  # noqa: E731
+                                      dtype=torch.bfloat16)
+    blocks = -(-n // 16)
+    q, k = rand(n, hq, d), rand(blocks, hkv, 16, d)
+    table = torch.randperm(blocks, generator=g, device="cuda").int()[None].contiguous()
+    scale = float(np.float32(d ** -0.5))
+    rows = k[table[0].long()].transpose(1, 2).reshape(-1, hkv, d)[:n].double()
+    later = torch.ones((n, n), dtype=torch.bool, device="cuda").triu(1)
+    want = torch.zeros((hkv, n), dtype=torch.float64, device="cuda")
+    lse = torch.empty((n, hq), device="cuda")
+    for h in range(hq):
+        x = (q[:, h].double() @ rows[:, h // (hq // hkv)].T * scale).masked_fill(later, -float("inf"))
+        lse[:, h] = torch.logsumexp(x, -1).float()
+        want[h // (hq // hkv)] += torch.exp(x - lse[:, h, None].double()).sum(0)
+    got = pa().pa_attention_mass(q, lse, H.dev_i32([0, n]), n, k, table, H.dev_i32([n]), scale)
+    err = (got[0, :, :n].double() - want).abs()
+    assert bool((err <= (8e-5 + n * (hq // hkv) / 2 * 2.0 ** -24) * want).all())
+    assert not bool(got[0, :, n:].any()) and pa().pa_get_device_error() == 0

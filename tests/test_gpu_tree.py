@@ -412,3 +412,32 @@ def test_outputs_are_rounded_both_ways_alike():
     off = (out.double() - nearest.double()) * want.sign()
     low, high = int((off < 0).sum()), int((off > 0).sum())
     assert abs(low - high) <= 5 * (low + high) ** 0.5 + 2.0 ** -11 * want.numel(), (low, high)
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(16, 1, 64), (4, 4, 128)])
+def test_the_most_drafted_tokens(hq, hkv, d):
+    # 4096 of them (256 passes at group 16), any bits; some rows against 64 bits
+    import torch
+    n, c = 4096, 104
+    L = n + c
+    g = torch.Generator(device="cuda").manual_seed(hq)
+    rand = lambda *shape: torch.randn(shape, generator=g, device="cuda",  # noqa: E731
+                                      dtype=torch.bfloat16)
+    blocks = -(-L // 16)
+    q, k, v = rand(n, hq, d), rand(blocks + 5, hkv, 16, d), rand(blocks + 5, hkv, 16, d)
+    table = torch.randperm(blocks + 5, generator=g, device="cuda")[:blocks].int()[None]
+    mask = torch.randint(-2 ** 63, 2 ** 63 - 1, (n, 64), generator=g, device="cuda")
+    out, lse = pa().pa_tree_attention(q, H.dev_i32([0, n]), n, mask, k, v, table.contiguous(),
+                                      H.dev_i32([L]), d ** -0.5, want_lse=True)
+    rows = torch.randperm(n, generator=g, device="cuda")[:96]
+    rows[:2] = torch.tensor([0, n - 1], device="cuda")
+    flat = lambda pool: pool[table[0].long()].transpose(1, 2).reshape(-1, hkv, d)[:L].double()  # noqa: E731
+    x = torch.einsum("ihgd,thd->ihgt", q[rows].double().view(-1, hkv, hq // hkv, d), flat(k))
+    j = torch.arange(n, device="cuda")
+    see = ((mask[rows][:, j // 64] >> (j % 64)) & 1).bool()
+    see = torch.cat([torch.ones((len(rows), c), dtype=torch.bool, device="cuda"), see], 1)
+    x = (x * float(np.float32(d ** -0.5))).masked_fill(~see[:, None, None], -float("inf"))
+    e = torch.logsumexp(x, -1)
+    o = torch.einsum("ihgt,thd->ihgd", torch.exp(x - e[..., None]), flat(v))
+    check(out[rows], lse[rows], (o.reshape(-1, hq, d).cpu().numpy(), e.reshape(-1, hq).cpu().numpy()))
+    assert pa().pa_get_device_error() == 0
