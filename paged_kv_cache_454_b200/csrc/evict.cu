@@ -633,6 +633,9 @@ __global__ void __launch_bounds__(kMoveThreads) move_out_kernel(const __grid_con
 
 // In place: blockIdx.x = ((sequence, head), slice); a slice is four 16-byte
 // chunks of K's or V's rows.  Thread i of a turn takes rows i / 4, + 64, ...
+// Measured with the choice: 48 sequences brought down to 1531 tokens 157 us (into other
+// blocks 123), one of 31337 to 4096 57 us (19): a (sequence, head) has eight CTAs at
+// D = 128, and a turn is a chain of dependent loads (list, table, row).
 constexpr int kPlaceThreads = 256;
 constexpr int kSliceLanes = 4;
 constexpr int kPlaceUnroll = 4;
@@ -703,7 +706,7 @@ int run_move(MoveParams& p, int head_dim, bool dependent, cudaStream_t stream) {
   if (p.new_tables) {
     // enough CTAs to fill the device several times over, no more than the rows need
     const int cta_rows = move_cta_rows(head_dim);
-    const int64_t most = (p.kept_stride + cta_rows - 1) / cta_rows;
+    const int64_t most = (static_cast<int64_t>(p.kept_stride) + cta_rows - 1) / cta_rows;
     const int64_t want = (static_cast<int64_t>(num_sms()) * 64 + rows - 1) / rows;
     p.parts = static_cast<int>(std::max<int64_t>(1, std::min(most, want)));
     if (rows * p.parts > 0x7fffffff) return PA_ERR_UNSUPPORTED;

@@ -21,11 +21,11 @@
 // A stream has two buffers of scores, one per half of a tile: while the softmax
 // works on one half, the other's weights are multiplied and the half after that
 // is scored (with one buffer of a whole tile, scores, softmax and product follow
-// each other and the tensor cores idle half the time: 533 against 404 us on 48
-// sequences).  K and V have five slots of a tile at D = 128 (four: 111 against 96
-// us on 24 sequences of 32/32 heads, 480 against 407 on 48 of 64/8).  A thread takes its 64 scores into registers once and puts the
-// weights back once: tensor memory answers between products, so every round trip
-// to it waits.
+// each other and the tensor cores idle half the time).  K and V have five slots of a
+// tile at D = 128 (four: 111 against 96 us on 24 sequences of 32/32 heads, 480 against
+// 407 on 48 of 64/8).  A thread takes its 64 scores into registers once and puts the
+// weights back once: tensor memory answers between products, so every round trip to it
+// waits.
 //
 // Work split: all items' key tiles, in order, are one line, on which a tile has
 // places for its time and an item more in front of them for what it costs besides,
@@ -35,8 +35,12 @@
 // rows and base-2 log-sum-exps in the workspace -- at most two items per CTA --
 // and a second kernel, a programmatic dependent, merges them.
 //
-// Bound: HBM (K and V are read once per pass) up to about 128 rows of a KV head;
-// the tensor cores and the softmax warps beyond.
+// Bound: for many rows the tensor cores (48 sequences of 64/8 heads and 7 to 63 drafted
+// tokens over 300 to 16001: 406 to 430 us, 711 TFLOP/s without P_lo; their pipe is busy
+// for 62% of the active cycles); for few the padding of their 128-row tiles (24
+// sequences of 32/32 heads, 3 to 25 drafted: 95 us against 43 of HBM; tensor pipe 32%,
+// DRAM 37%, one softmax warp of four at work); for one sequence the latency of two
+// kernels (17 to 19 us).
 //
 // Roles (one CTA per SM): warp 0 copies K and V pages (one ring, K and V of a
 // tile in turn), warps 1 and 2 issue the MMAs of one stream each (one warp for
@@ -60,8 +64,11 @@ using namespace tc;
 
 constexpr int kThreads = 384;
 constexpr int kMaxCtas = 160;      // partial results are sized for this many
-// Places on the line, from a fit of the CTAs' cycles to what they had (a tile 3100
-// to 3500 in split mode, 3700 in pair mode; an item 4200 and 12700 besides).
+// Places on the line, near a fit of the CTAs' cycles to what they had, over six batches
+// (a tile 3570 in split mode, 3950 in pair mode; an item 4100 and 12100 besides).  Five
+// other ratios, the fit's own (9, 10; 10, 30) among them, time alike on seven batches
+// within two runs' scatter: 93 to 98 us on 24 sequences of 32/32 heads and 358 to 403 on
+// 48 of 64/8, these 93 to 94 and 361 to 366.
 constexpr int kSplitTile = 5, kPairTile = 6;
 constexpr int kSplitItem = 7, kPairItem = 22;  // in front of an item's tiles
 constexpr int kMinPlaces = 10;                 // of a stretch
